@@ -12,6 +12,8 @@ from ._lib import (  # noqa: F401
     bwd_workspace_size, partition, score_select, build_plan, attn_fwd, attn_bwd, get_status,
     decode_stats, default_scale, kernel_launches, trace_enable, trace_read, score_select_static,
     score_select_variant, SELECT_VARIANTS, HEAD_STATS_DTYPE,
+    NormRope, Act8, rope_dims, rope_table, qk_norm_rope, qk_norm_rope_partition,
+    qk_norm_rope_bwd, qk_norm_rope_bwd_workspace_size, act8_pack, act8_unpack,
 )
 
 __all__ = [
@@ -19,4 +21,6 @@ __all__ = [
     "bwd_workspace_size", "partition", "score_select", "build_plan", "attn_fwd", "attn_bwd",
     "get_status", "decode_stats", "default_scale", "kernel_launches", "trace_enable", "trace_read",
     "score_select_static", "score_select_variant", "SELECT_VARIANTS", "HEAD_STATS_DTYPE",
+    "NormRope", "Act8", "rope_dims", "rope_table", "qk_norm_rope", "qk_norm_rope_partition",
+    "qk_norm_rope_bwd", "qk_norm_rope_bwd_workspace_size", "act8_pack", "act8_unpack",
 ]

@@ -4,9 +4,11 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 
 #include "common.cuh"
 #include "pairs.cuh"
+#include "rows.cuh"
 
 using namespace vmoba;
 
@@ -305,6 +307,210 @@ int vmoba_attn_bwd(const vmoba_shape* shape, const void* q, const void* k_perm,
   return cuda_status(launch_attn_bwd_simt(P, q, k_perm, v_perm, sel_bits, ws, L, scale, lse,
                                           dout, dq, dk, dv, static_cast<float*>(ws_bwd),
                                           stream));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Around the attention: norm + rotation, 8-bit checkpoints.
+// ---------------------------------------------------------------------------
+
+namespace {
+
+bool all_aligned(std::initializer_list<const void*> ptrs) {
+  for (const void* p : ptrs)
+    if (!p || !aligned16(p)) return false;
+  return true;
+}
+
+// ld of raw rows: room for one kind's heads, 16-byte vectors.
+bool good_ld(const Prob& P, long long ld) {
+  const int e = P.dtype == VMOBA_BF16 ? 2 : 4;
+  return ld >= (long long)P.n_h * P.d && ld <= (1LL << 40) && (ld * e) % 16 == 0;
+}
+
+bool good_dims(const Prob& P, int dt, int dh, int dw) {
+  const int most = P.d;
+  return dt >= 0 && dh >= 0 && dw >= 0 && dt <= most && dh <= most && dw <= most &&
+         dt + dh + dw <= most && dt % 2 == 0 && dh % 2 == 0 && dw % 2 == 0;
+}
+
+int norm_rope_args(const Prob& P, const vmoba_norm_rope* nr, NormRopeArgs* a) {
+  if (!nr) return VMOBA_ERR_ARG;
+  if (!good_dims(P, nr->dim_t, nr->dim_h, nr->dim_w)) return VMOBA_ERR_SHAPE;
+  if (!(nr->eps >= 1e-30f) || std::isinf(nr->eps)) return VMOBA_ERR_ARG;
+  if (nr->dim_t + nr->dim_h + nr->dim_w > 0 && !nr->table) return VMOBA_ERR_ARG;
+  if (!aligned16(nr->table) || !aligned16(nr->q_weight) || !aligned16(nr->k_weight))
+    return VMOBA_ERR_ARG;
+  NormRopeArgs n{};
+  n.gq = nr->q_weight; n.gk = nr->k_weight; n.eps = nr->eps;
+  n.table = reinterpret_cast<const float2*>(nr->table);
+  n.ht = nr->dim_t / 2; n.hh = nr->dim_h / 2; n.hw = nr->dim_w / 2;
+  *a = n;
+  return VMOBA_OK;
+}
+
+// The forward: from raw rows (codes null) or from a checkpoint.
+int norm_rope_fwd(const vmoba_shape* shape, const vmoba_norm_rope* nr, const void* q_in,
+                  const void* k_in, const void* v_in, long long ld, const int8_t* codes,
+                  const float* scales, bool from8, void* q, void* k, void* v, float* blocks,
+                  bool partition, int8_t* ckpt_codes, float* ckpt_scales, cudaStream_t stream) {
+  Prob P;
+  NormRopeArgs a;
+  int rc = make_prob(shape, &P);
+  if (rc != VMOBA_OK) return rc;
+  if ((rc = norm_rope_args(P, nr, &a)) != VMOBA_OK) return rc;
+  if (from8) {
+    if (!all_aligned({codes, scales})) return VMOBA_ERR_ARG;
+    a.codes = codes; a.scales = scales;
+  } else {
+    if (!all_aligned({q_in, k_in, v_in}) || !good_ld(P, ld)) return VMOBA_ERR_ARG;
+    a.in[0] = q_in; a.in[1] = k_in; a.in[2] = v_in; a.ld = ld;
+  }
+  if (!all_aligned({q, k, v}) || (partition && !all_aligned({blocks}))) return VMOBA_ERR_ARG;
+  if ((ckpt_codes || ckpt_scales) && !all_aligned({ckpt_codes, ckpt_scales})) return VMOBA_ERR_ARG;
+  const NormRopeOut o{q, k, v, partition ? blocks : nullptr, ckpt_codes, ckpt_scales};
+  drop_stale_error();
+  return cuda_status(launch_norm_rope(P, a, o, stream));
+}
+
+int norm_rope_bwd(const vmoba_shape* shape, const vmoba_norm_rope* nr, const void* q_in,
+                  const void* k_in, long long ld, const int8_t* codes, const float* scales,
+                  bool from8, const void* dq, const void* dk, const void* dv, void* dq_in,
+                  void* dk_in, void* dv_in, long long ld_out, float* dweight, void* ws,
+                  size_t ws_bytes, cudaStream_t stream) {
+  Prob P;
+  NormRopeArgs a;
+  int rc = make_prob(shape, &P);
+  if (rc != VMOBA_OK) return rc;
+  if ((rc = norm_rope_args(P, nr, &a)) != VMOBA_OK) return rc;
+  if (from8) {
+    if (!all_aligned({codes, scales})) return VMOBA_ERR_ARG;
+    a.codes = codes; a.scales = scales;
+  } else {
+    if (!all_aligned({q_in, k_in}) || !good_ld(P, ld)) return VMOBA_ERR_ARG;
+    a.in[0] = q_in; a.in[1] = k_in; a.ld = ld;
+  }
+  if (!all_aligned({dq, dk, dv, dq_in, dk_in, dv_in}) || !good_ld(P, ld_out)) return VMOBA_ERR_ARG;
+  if (dweight) {
+    if (!aligned16(dweight)) return VMOBA_ERR_ARG;
+    if (!ws || !aligned16(ws) || ws_bytes < norm_rope_bwd_ws_bytes(P)) return VMOBA_ERR_WORKSPACE;
+  }
+  void* const out[3] = {dq_in, dk_in, dv_in};
+  drop_stale_error();
+  return cuda_status(
+      launch_norm_rope_bwd(P, a, dq, dk, dv, out, ld_out, dweight, ws, num_sms(), stream));
+}
+
+// Shared checks of the 8-bit passes; *none is set when there is nothing to do.
+int check_act8(int dtype, const void* x, long long rows, int cols, long long ld, int group,
+               const void* codes, const void* scales, bool* none) {
+  if (dtype != VMOBA_BF16 && dtype != VMOBA_F32) return VMOBA_ERR_DTYPE;
+  if (rows < 0 || cols < 1 || ld < cols || ld > (1LL << 40) || (group != 64 && group != 128))
+    return VMOBA_ERR_SHAPE;
+  const long long per_row = ((long long)cols + group - 1) / group;
+  if (rows >= (1LL << 34) / per_row) return VMOBA_ERR_SHAPE;
+  *none = rows == 0;
+  if (*none) return VMOBA_OK;
+  if (ld > (1LL << 60) / rows) return VMOBA_ERR_SHAPE;      // byte offsets stay within 64 bits
+  const uintptr_t e = dtype == VMOBA_BF16 ? 2 : 4;
+  if (!x || !codes || !scales) return VMOBA_ERR_ARG;
+  if (reinterpret_cast<uintptr_t>(x) % e || reinterpret_cast<uintptr_t>(scales) % 4)
+    return VMOBA_ERR_ARG;
+  return VMOBA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int vmoba_rope_table(const vmoba_shape* shape, int dim_t, int dim_h, int dim_w, double base,
+                     long long origin_t, long long origin_h, long long origin_w, float* table,
+                     cudaStream_t stream) {
+  Prob P;
+  int rc = make_prob(shape, &P);
+  if (rc != VMOBA_OK) return rc;
+  if (!good_dims(P, dim_t, dim_h, dim_w)) return VMOBA_ERR_SHAPE;
+  if (!(base > 0.0) || std::isinf(base)) return VMOBA_ERR_ARG;
+  const long long origin[3] = {origin_t, origin_h, origin_w};
+  for (long long o : origin)
+    if (o < -(1LL << 31) || o > (1LL << 31)) return VMOBA_ERR_ARG;
+  if (dim_t + dim_h + dim_w == 0) return VMOBA_OK;
+  if (!table || !aligned16(table)) return VMOBA_ERR_ARG;
+  drop_stale_error();
+  return cuda_status(launch_rope_table(P.T, P.H, P.W, dim_t / 2, dim_h / 2, dim_w / 2, base,
+                                       origin, reinterpret_cast<float2*>(table), stream));
+}
+
+int vmoba_qk_norm_rope(const vmoba_shape* shape, const vmoba_norm_rope* nr, const void* q_in,
+                       const void* k_in, const void* v_in, long long ld, void* q, void* k,
+                       void* v, int8_t* ckpt_codes, float* ckpt_scales, cudaStream_t stream) {
+  return norm_rope_fwd(shape, nr, q_in, k_in, v_in, ld, nullptr, nullptr, false, q, k, v, nullptr,
+                       false, ckpt_codes, ckpt_scales, stream);
+}
+
+int vmoba_qk_norm_rope_partition(const vmoba_shape* shape, const vmoba_norm_rope* nr,
+                                 const void* q_in, const void* k_in, const void* v_in,
+                                 long long ld, void* q, void* k_perm, void* v_perm, float* blocks,
+                                 int8_t* ckpt_codes, float* ckpt_scales, cudaStream_t stream) {
+  return norm_rope_fwd(shape, nr, q_in, k_in, v_in, ld, nullptr, nullptr, false, q, k_perm,
+                       v_perm, blocks, true, ckpt_codes, ckpt_scales, stream);
+}
+
+int vmoba_qk_norm_rope_act8(const vmoba_shape* shape, const vmoba_norm_rope* nr,
+                            const int8_t* codes, const float* scales, void* q, void* k, void* v,
+                            cudaStream_t stream) {
+  return norm_rope_fwd(shape, nr, nullptr, nullptr, nullptr, 0, codes, scales, true, q, k, v,
+                       nullptr, false, nullptr, nullptr, stream);
+}
+
+int vmoba_qk_norm_rope_partition_act8(const vmoba_shape* shape, const vmoba_norm_rope* nr,
+                                      const int8_t* codes, const float* scales, void* q,
+                                      void* k_perm, void* v_perm, float* blocks,
+                                      cudaStream_t stream) {
+  return norm_rope_fwd(shape, nr, nullptr, nullptr, nullptr, 0, codes, scales, true, q, k_perm,
+                       v_perm, blocks, true, nullptr, nullptr, stream);
+}
+
+size_t vmoba_qk_norm_rope_bwd_workspace_size(const vmoba_shape* shape) {
+  Prob P;
+  return make_prob(shape, &P) == VMOBA_OK ? norm_rope_bwd_ws_bytes(P) : 0;
+}
+
+int vmoba_qk_norm_rope_bwd(const vmoba_shape* shape, const vmoba_norm_rope* nr, const void* q_in,
+                           const void* k_in, long long ld, const void* dq, const void* dk,
+                           const void* dv, void* dq_in, void* dk_in, void* dv_in,
+                           long long ld_out, float* dweight, void* ws, size_t ws_bytes,
+                           cudaStream_t stream) {
+  return norm_rope_bwd(shape, nr, q_in, k_in, ld, nullptr, nullptr, false, dq, dk, dv, dq_in,
+                       dk_in, dv_in, ld_out, dweight, ws, ws_bytes, stream);
+}
+
+int vmoba_qk_norm_rope_bwd_act8(const vmoba_shape* shape, const vmoba_norm_rope* nr,
+                                const int8_t* codes, const float* scales, const void* dq,
+                                const void* dk, const void* dv, void* dq_in, void* dk_in,
+                                void* dv_in, long long ld_out, float* dweight, void* ws,
+                                size_t ws_bytes, cudaStream_t stream) {
+  return norm_rope_bwd(shape, nr, nullptr, nullptr, 0, codes, scales, true, dq, dk, dv, dq_in,
+                       dk_in, dv_in, ld_out, dweight, ws, ws_bytes, stream);
+}
+
+int vmoba_act8_pack(int dtype, const void* x, long long rows, int cols, long long ld, int group,
+                    int8_t* codes, float* scales, cudaStream_t stream) {
+  bool none = false;
+  const int rc = check_act8(dtype, x, rows, cols, ld, group, codes, scales, &none);
+  if (rc != VMOBA_OK || none) return rc;
+  drop_stale_error();
+  return cuda_status(launch_act8_pack(dtype, x, rows, cols, ld, group, codes, scales, stream));
+}
+
+int vmoba_act8_unpack(int dtype, const int8_t* codes, const float* scales, long long rows,
+                      int cols, int group, void* out, long long ld, cudaStream_t stream) {
+  bool none = false;
+  const int rc = check_act8(dtype, out, rows, cols, ld, group, codes, scales, &none);
+  if (rc != VMOBA_OK || none) return rc;
+  drop_stale_error();
+  return cuda_status(launch_act8_unpack(dtype, codes, scales, rows, cols, group, out, ld, stream));
 }
 
 int vmoba_get_status(void* ws, int* device_status, cudaStream_t stream) {

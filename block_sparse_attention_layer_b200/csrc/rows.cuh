@@ -1,0 +1,303 @@
+// Rows of one head in registers, shared by the kernels around the attention
+// (norm + rotation forward and backward, 8-bit checkpoints).
+//
+// A row of D elements (64 or 128) lies over G = D / 8 neighbouring lanes,
+// eight elements a lane, so a warp holds R = 32 / G rows.  bf16: elements
+// 8 l .. 8 l + 7 (one 16-byte access).  fp32: 4 l .. 4 l + 3 and the same in
+// the row's second half (two 16-byte accesses, each contiguous over the
+// lanes).  Adjacent elements (2p, 2p + 1) always share a lane.
+//
+// 8-bit checkpoints: a group of values with a = max |x| is stored as codes
+// round-half-even(127 x / a) of the exact quotient and the fp32 scale a / 127;
+// it reads back as code * scale, off by at most a / 254 (+ the rounding of
+// the scale).  A group with an infinity or NaN gets a NaN scale and reads back
+// as NaN throughout; one with a < 2^-119 (whose scale would be subnormal) is
+// stored as zeros.
+#pragma once
+
+#include "common.cuh"
+
+namespace vmoba {
+namespace rows {
+
+constexpr unsigned kAll = 0xFFFFFFFFu;
+
+template <typename E>
+struct Raw;  // a lane's eight elements as loaded
+template <>
+struct Raw<__nv_bfloat16> { uint4 u; };
+template <>
+struct Raw<float> { float4 a, b; };
+
+// Element i (0..7) of lane l within the row.
+template <typename E, int D>
+__device__ __forceinline__ int elem_at(int l, int i) {
+  if (sizeof(E) == 2) return l * 8 + i;
+  return i < 4 ? l * 4 + i : D / 2 + l * 4 + i - 4;
+}
+
+template <int D>
+__device__ __forceinline__ Raw<__nv_bfloat16> load_row(const __nv_bfloat16* row, int l) {
+  return {__ldg(reinterpret_cast<const uint4*>(row) + l)};
+}
+template <int D>
+__device__ __forceinline__ Raw<float> load_row(const float* row, int l) {
+  const float4* p = reinterpret_cast<const float4*>(row);
+  return {__ldg(p + l), __ldg(p + D / 8 + l)};
+}
+
+template <int D>
+__device__ __forceinline__ void store_raw(__nv_bfloat16* row, int l, const Raw<__nv_bfloat16>& r) {
+  reinterpret_cast<uint4*>(row)[l] = r.u;
+}
+template <int D>
+__device__ __forceinline__ void store_raw(float* row, int l, const Raw<float>& r) {
+  float4* p = reinterpret_cast<float4*>(row);
+  p[l] = r.a;
+  p[D / 8 + l] = r.b;
+}
+
+__device__ __forceinline__ void unpack(const Raw<__nv_bfloat16>& r, float (&x)[8]) {
+  const uint32_t w[4] = {r.u.x, r.u.y, r.u.z, r.u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void unpack(const Raw<float>& r, float (&x)[8]) {
+  x[0] = r.a.x; x[1] = r.a.y; x[2] = r.a.z; x[3] = r.a.w;
+  x[4] = r.b.x; x[5] = r.b.y; x[6] = r.b.z; x[7] = r.b.w;
+}
+
+// The one rounding of a result: to the storage type, nearest even.
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+__device__ __forceinline__ void pack(const float (&x)[8], Raw<__nv_bfloat16>& r) {
+  r.u = make_uint4(bf16x2(x[0], x[1]), bf16x2(x[2], x[3]), bf16x2(x[4], x[5]),
+                   bf16x2(x[6], x[7]));
+}
+__device__ __forceinline__ void pack(const float (&x)[8], Raw<float>& r) {
+  r.a = make_float4(x[0], x[1], x[2], x[3]);
+  r.b = make_float4(x[4], x[5], x[6], x[7]);
+}
+
+// Sum over the G lanes of a row (every lane of the warp takes part).
+template <int G>
+__device__ __forceinline__ float row_sum(float v) {
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+  return v;
+}
+template <int G>
+__device__ __forceinline__ uint32_t row_max(uint32_t v) {
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(kAll, v, o));
+  return v;
+}
+
+// ---- 8-bit groups ----
+
+// The lane's part of max |x| as ordered bits (an infinity or NaN sorts above
+// every finite value).
+__device__ __forceinline__ uint32_t abs_max_bits(const float (&x)[8]) {
+  uint32_t m = 0u;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+  return m;
+}
+
+// Codes of a lane's eight values, byte i = element i, for a group whose
+// max |x| has the bits `m`; scale gets the group's.  The quotient is taken
+// as x * (127 / a) in fp32 (within 2^-16 absolute of the exact one) and
+// rounded by adding 1.5 * 2^23; a value that lands within 2e-5 of a rounding
+// border, where that error could decide, is redone in fp64 with a correctly
+// rounded division, whose quotient is exact enough for every bf16 and fp32
+// input to fall on the right side.
+__device__ __forceinline__ uint2 encode8(const float (&x)[8], uint32_t m, float& scale) {
+  const float a = __uint_as_float(m);
+  if (m >= 0x7F800000u || a < 0x1p-119f) {
+    scale = m >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : 0.f;
+    return make_uint2(0u, 0u);
+  }
+  scale = a / 127.0f;
+  const float inv = 127.0f / a;
+  constexpr float kMagic = 12582912.0f;
+  uint32_t w[8];
+  float border = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float y = x[i] * inv;
+    const float z = y + kMagic;
+    border = fmaxf(border, fabsf(y - (z - kMagic)));
+    w[i] = __float_as_uint(z);
+  }
+  if (border > 0.49998f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      w[i] = (uint32_t)(int)rint((double)x[i] * 127.0 / (double)a);
+  }
+  const uint32_t lo = __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040),
+                                  0x5410);
+  const uint32_t hi = __byte_perm(__byte_perm(w[4], w[5], 0x0040), __byte_perm(w[6], w[7], 0x0040),
+                                  0x5410);
+  return make_uint2(lo, hi);
+}
+
+// code * scale of eight codes, exact integers times the fp32 scale (one
+// rounding).  A byte c + 128 in the mantissa of 2^23 is 2^23 + 128 + c.
+__device__ __forceinline__ void decode8(uint2 c, float scale, float (&x)[8]) {
+  const uint32_t w[2] = {c.x ^ 0x80808080u, c.y ^ 0x80808080u};
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    x[i] = (__uint_as_float(__byte_perm(w[i >> 2], 0x4B000000u, 0x7440 + (i & 3))) - 8388736.0f) *
+           scale;
+}
+
+// A lane's eight codes of a row of D codes, in the element order of E.
+template <typename E, int D>
+__device__ __forceinline__ uint2 load_codes(const int8_t* row, int l) {
+  if (sizeof(E) == 2) return __ldg(reinterpret_cast<const uint2*>(row) + l);
+  const uint32_t* p = reinterpret_cast<const uint32_t*>(row);
+  return make_uint2(__ldg(p + l), __ldg(p + D / 8 + l));
+}
+template <typename E, int D>
+__device__ __forceinline__ void store_codes(int8_t* row, int l, uint2 c) {
+  if (sizeof(E) == 2) {
+    reinterpret_cast<uint2*>(row)[l] = c;
+  } else {
+    uint32_t* p = reinterpret_cast<uint32_t*>(row);
+    p[l] = c.x;
+    p[D / 8 + l] = c.y;
+  }
+}
+
+// ---- norm ----
+
+// 1 / sqrt(mean x^2 + eps) of a row from the lane's eight elements.  Where
+// the squares leave fp32's range the row is first scaled by pre = 2^-80 (x
+// changes; eps then is far below the mean's last bit); else pre = 1.
+template <int D>
+__device__ __forceinline__ float inv_rms(float (&x)[8], float eps, float& pre) {
+  constexpr int G = D / 8;
+  float ss = 0.f;
+  pre = 1.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+  ss = row_sum<G>(ss);
+  const bool big = !(ss < 0x1p100f);
+  if (__any_sync(kAll, big)) {
+    float t = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (big) x[i] *= 0x1p-80f;
+      t = fmaf(x[i], x[i], t);
+    }
+    t = row_sum<G>(t);
+    if (big) { ss = t; eps = 0.f; pre = 0x1p-80f; }
+  }
+  return rsqrtf(fmaf(ss, 1.0f / D, eps));
+}
+
+// ---- rotation ----
+
+// The table entries that a lane's four pairs read: entry = base + stride *
+// position on the pair's axis (0, 1, 2 = t, y, x; 3 = the pair stays).
+struct PairRefs {
+  int base[4], stride[4], axis[4];
+};
+
+template <typename E, int D>
+__device__ __forceinline__ PairRefs pair_refs(int l, int T, int H, int ht, int hh, int hw) {
+  PairRefs r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    int p = elem_at<E, D>(l, 2 * i) / 2;
+    if (p < ht) {
+      r.axis[i] = 0; r.base[i] = p; r.stride[i] = ht;
+    } else if ((p -= ht) < hh) {
+      r.axis[i] = 1; r.base[i] = T * ht + p; r.stride[i] = hh;
+    } else if ((p -= hh) < hw) {
+      r.axis[i] = 2; r.base[i] = T * ht + H * hh + p; r.stride[i] = hw;
+    } else {
+      r.axis[i] = 3; r.base[i] = 0; r.stride[i] = 0;
+    }
+  }
+  return r;
+}
+
+__device__ __forceinline__ void load_turns(const PairRefs& r, const float2* table, int t, int y,
+                                           int x, float2 (&cs)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int pos = r.axis[i] == 0 ? t : (r.axis[i] == 1 ? y : x);
+    cs[i] = make_float2(1.f, 0.f);
+    if (r.axis[i] < 3) cs[i] = __ldg(table + r.base[i] + r.stride[i] * pos);
+  }
+}
+
+// (y0, y1) -> (y0 c - y1 s, y0 s + y1 c)
+__device__ __forceinline__ void turn(float (&x)[8], const float2 (&cs)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float a = x[2 * i], b = x[2 * i + 1];
+    x[2 * i] = fmaf(a, cs[i].x, -(b * cs[i].y));
+    x[2 * i + 1] = fmaf(a, cs[i].y, b * cs[i].x);
+  }
+}
+// the transpose (= the inverse)
+__device__ __forceinline__ void turn_back(float (&x)[8], const float2 (&cs)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float a = x[2 * i], b = x[2 * i + 1];
+    x[2 * i] = fmaf(a, cs[i].x, b * cs[i].y);
+    x[2 * i + 1] = fmaf(b, cs[i].x, -(a * cs[i].y));
+  }
+}
+
+// A lane's eight weights of a row (ones where there are none).
+template <typename E, int D>
+__device__ __forceinline__ void load_weights(const float* g, int l, float (&w)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = g ? __ldg(g + elem_at<E, D>(l, i)) : 1.f;
+}
+
+}  // namespace rows
+
+// What the norm + rotation kernels are given, besides the layer's geometry.
+struct NormRopeArgs {
+  const void* in[3];          // raw q, k, v: [s] rows of n_h * d, `ld` elements apart
+  long long ld;
+  const int8_t* codes;        // or their 8-bit checkpoint [s][3][n_h][d] ...
+  const float* scales;        // ... with a scale for each row of d: [s][3][n_h]
+  const float *gq, *gk;       // norm weights [d], or null
+  float eps;
+  const float2* table;        // (cos, sin): T * ht, then H * hh, then W * hw entries
+  int ht, hh, hw;             // pairs that turn with t, y, x
+};
+
+struct NormRopeOut {
+  void *q, *k, *v;
+  float* blocks;              // block means of k ([n_h][N_b][d]), or null: k, v in token order
+  int8_t* codes;              // checkpoint to write, or null
+  float* scales;
+};
+
+cudaError_t launch_norm_rope(const Prob& P, const NormRopeArgs& a, const NormRopeOut& o,
+                             cudaStream_t st);
+size_t norm_rope_bwd_ws_bytes(const Prob& P);
+cudaError_t launch_norm_rope_bwd(const Prob& P, const NormRopeArgs& a, const void* dq,
+                                 const void* dk, const void* dv, void* const (&out)[3],
+                                 long long ld_out, float* dweight, void* ws, int num_sms,
+                                 cudaStream_t st);
+cudaError_t launch_rope_table(int T, int H, int W, int ht, int hh, int hw, double base,
+                              const long long (&origin)[3], float2* table, cudaStream_t st);
+cudaError_t launch_act8_pack(int dtype, const void* x, long long n_rows, int cols, long long ld,
+                             int group, int8_t* codes, float* scales, cudaStream_t st);
+cudaError_t launch_act8_unpack(int dtype, const int8_t* codes, const float* scales,
+                               long long n_rows, int cols, int group, void* out, long long ld,
+                               cudaStream_t st);
+
+}  // namespace vmoba

@@ -310,6 +310,113 @@ int vmoba_score_select_static(const vmoba_shape* shape, const void* q, const flo
                               float tau, float scale, uint32_t* sel_bits,
                               vmoba_head_stats* stats, cudaStream_t stream);
 
+/* ---- Around the attention: norm + rotation, 8-bit checkpoints ----
+ *
+ * Between the projection and the attention a video DiT normalises each
+ * head's query and key and rotates them by the token's position:
+ *   norm:      y_i = x_i g_i / sqrt(mean_j x_j^2 + eps) over the head_dim
+ *              values of one token and head;
+ *   rotation:  the adjacent pairs (2p, 2p+1) turn by the angle
+ *              (origin + position) * base^(-2i / dim): the first dim_t / 2
+ *              pairs with t, the next dim_h / 2 with y, the next dim_w / 2
+ *              with x (i counts within the axis), the rest stay:
+ *              (y0, y1) -> (y0 cos - y1 sin, y0 sin + y1 cos).
+ * The arithmetic is fp32; each result is rounded to dtype once.  Raw rows: q,
+ * k, v point at token 0's first head of each; head h is head_dim elements
+ * further per head, token n is ld elements further per token (ld >= n_heads *
+ * head_dim): the packed output of one projection ([s][3][n_heads][head_dim],
+ * k = q + n_heads * head_dim, ld = 3 * n_heads * head_dim or more) or three
+ * separate ones (ld = n_heads * head_dim).  Every pointer 16-byte aligned, ld
+ * a multiple of 16 bytes.  Outputs must not overlap inputs. */
+typedef struct vmoba_norm_rope {
+  const float* q_weight;      /* [head_dim] fp32 device, or NULL (all ones) */
+  const float* k_weight;
+  float eps;                  /* finite, >= 1e-30 */
+  const float* table;         /* from vmoba_rope_table; may be NULL if no pair turns */
+  int dim_t, dim_h, dim_w;    /* even, >= 0, sum <= head_dim */
+} vmoba_norm_rope;
+
+/* Fills the rotation table of the shape's grid: (cos, sin) pairs, fp32, of
+ * T * dim_t / 2, then H * dim_h / 2, then W * dim_w / 2 (position, pair)
+ * entries; the angles are formed in fp64.  base > 0 and finite; the origins'
+ * magnitude at most 2^31.  table: 16-byte aligned, 4 * (T * dim_t + H * dim_h +
+ * W * dim_w) bytes; may be NULL if that is 0. */
+int vmoba_rope_table(const vmoba_shape* shape, int dim_t, int dim_h, int dim_w, double base,
+                     long long origin_t, long long origin_h, long long origin_w, float* table,
+                     cudaStream_t stream);
+
+/* Forward in token order: q, k normalised and rotated, v copied, each
+ * [s][n_heads][head_dim] (what dense attention takes).  If ckpt_codes is not
+ * NULL the same pass stores the raw q, k, v as an 8-bit checkpoint: ckpt_codes
+ * [s][3][n_heads][head_dim] int8, ckpt_scales [s][3][n_heads] fp32 (one group
+ * is a head's row; see vmoba_act8_pack for its arithmetic). */
+int vmoba_qk_norm_rope(const vmoba_shape* shape, const vmoba_norm_rope* nr, const void* q_in,
+                       const void* k_in, const void* v_in, long long ld, void* q, void* k,
+                       void* v, int8_t* ckpt_codes, float* ckpt_scales, cudaStream_t stream);
+
+/* The same into the sparse layer's buffers, in place of vmoba_partition: q in
+ * token order, k_perm, v_perm [n_heads][s][head_dim] in partition order, and
+ * blocks [n_heads][N_b][head_dim], the fp32 means of each block's rotated keys
+ * before they are rounded to dtype (vmoba_partition, which is given rounded
+ * keys, takes the means of those). */
+int vmoba_qk_norm_rope_partition(const vmoba_shape* shape, const vmoba_norm_rope* nr,
+                                 const void* q_in, const void* k_in, const void* v_in,
+                                 long long ld, void* q, void* k_perm, void* v_perm,
+                                 float* blocks, int8_t* ckpt_codes, float* ckpt_scales,
+                                 cudaStream_t stream);
+
+/* Both, rebuilt from a checkpoint that an earlier forward stored: the raw q
+ * and k are code * scale in fp32 (not rounded to dtype), v is code * scale
+ * rounded to dtype. */
+int vmoba_qk_norm_rope_act8(const vmoba_shape* shape, const vmoba_norm_rope* nr,
+                            const int8_t* codes, const float* scales, void* q, void* k, void* v,
+                            cudaStream_t stream);
+int vmoba_qk_norm_rope_partition_act8(const vmoba_shape* shape, const vmoba_norm_rope* nr,
+                                      const int8_t* codes, const float* scales, void* q,
+                                      void* k_perm, void* v_perm, float* blocks,
+                                      cudaStream_t stream);
+
+/* Bytes of the backward's workspace (partial weight gradients), or 0 for an
+ * invalid shape. */
+size_t vmoba_qk_norm_rope_bwd_workspace_size(const vmoba_shape* shape);
+
+/* Backward.  dq, dk, dv: gradients of the rotated q, k and of v, [s][n_heads]
+ * [head_dim] (token order, as vmoba_attn_bwd writes them).  Writes the
+ * gradients of the raw rows in the layout of raw rows (dq_in, dk_in, dv_in,
+ * ld_out; dv_in is a copy of dv) and, if dweight is not NULL, the gradients of
+ * q_weight and k_weight, [2][head_dim] fp32 (for ones if the weight is NULL),
+ * summed in a fixed order.  The raw v is not needed.  ws:
+ * vmoba_qk_norm_rope_bwd_workspace_size bytes (may be NULL if dweight is), not
+ * shared by calls that may run at the same time. */
+int vmoba_qk_norm_rope_bwd(const vmoba_shape* shape, const vmoba_norm_rope* nr, const void* q_in,
+                           const void* k_in, long long ld, const void* dq, const void* dk,
+                           const void* dv, void* dq_in, void* dk_in, void* dv_in,
+                           long long ld_out, float* dweight, void* ws, size_t ws_bytes,
+                           cudaStream_t stream);
+
+/* The same with the raw q and k read from a checkpoint (code * scale). */
+int vmoba_qk_norm_rope_bwd_act8(const vmoba_shape* shape, const vmoba_norm_rope* nr,
+                                const int8_t* codes, const float* scales, const void* dq,
+                                const void* dk, const void* dv, void* dq_in, void* dk_in,
+                                void* dv_in, long long ld_out, float* dweight, void* ws,
+                                size_t ws_bytes, cudaStream_t stream);
+
+/* Activation checkpoints in 8 bits.  x: rows x cols values of dtype, rows ld
+ * elements apart (ld >= cols; any alignment of the type).  Groups of `group`
+ * (64 or 128) neighbouring columns, the last of a row possibly short: with a =
+ * max |x| of the group, codes = round-half-even(127 x / a) of the exact
+ * quotient, scales = a / 127 in fp32.  A group that holds an infinity or a NaN
+ * gets a NaN scale, one with a < 2^-119 a zero scale; their codes are zero.
+ * codes: [rows][cols] int8, scales: [rows][ceil(cols / group)] fp32, 4-byte
+ * aligned.  rows >= 0, cols >= 1, rows * ceil(cols / group) < 2^34. */
+int vmoba_act8_pack(int dtype, const void* x, long long rows, int cols, long long ld, int group,
+                    int8_t* codes, float* scales, cudaStream_t stream);
+
+/* out = code * scale in fp32, rounded to dtype: within a / 254 (and that
+ * rounding) of what was packed. */
+int vmoba_act8_unpack(int dtype, const int8_t* codes, const float* scales, long long rows,
+                      int cols, int group, void* out, long long ld, cudaStream_t stream);
+
 /* Number of CUDA kernels this library has launched since it was loaded
  * (host-side counter, thread-safe; diagnostics for launch accounting). */
 unsigned long long vmoba_kernel_launches(void);

@@ -1,0 +1,227 @@
+"""Host-side checks of the norm + rotation and 8-bit checkpoint calls: every
+refusal happens before anything is launched (no GPU needed), and the plain
+forms that the GPU tests compare with are themselves checked."""
+import ctypes
+
+import numpy as np
+import pytest
+
+import block_sparse_attention_layer_b200 as V
+from block_sparse_attention_layer_b200 import _lib
+
+from . import norm_rope_ref as R
+
+torch = pytest.importorskip("torch")
+
+OK = ctypes.c_void_p(0x100000)     # aligned, never dereferenced: the calls fail validation
+ODD = ctypes.c_void_p(0x100004)
+
+
+def _shape(**kw):
+    base = dict(T=4, H=8, W=8, n_heads=2, head_dim=64, mode=2, bt=2, bh=4, bw=4, dtype="bf16")
+    base.update(kw)
+    return V.LayerShape(**base)
+
+
+def _nr(eps=1e-6, table=0x100000, dims=(24, 20, 20), q=0, k=0):
+    return ctypes.byref(_lib.CNormRope(q, k, eps, table, *dims))
+
+
+def _sh(**kw):
+    return ctypes.byref(_shape(**kw).c())
+
+
+def _fwd(sh=None, nr=None, q_in=OK, ld=384, q=OK, blocks=OK, codes=None, scales=None):
+    return V.lib().vmoba_qk_norm_rope_partition(sh or _sh(), nr or _nr(), q_in, OK, OK, ld, q, OK,
+                                                OK, blocks, codes, scales, None)
+
+
+def _bwd(sh=None, nr=None, q_in=OK, ld=384, dq=OK, out=OK, ld_out=384, dw=OK, ws=OK,
+         n=1 << 30):
+    return V.lib().vmoba_qk_norm_rope_bwd(sh or _sh(), nr or _nr(), q_in, OK, ld, dq, OK, OK, out,
+                                          OK, OK, ld_out, dw, ws, n, None)
+
+
+@pytest.mark.parametrize("call", [_fwd, _bwd])
+@pytest.mark.parametrize("kw,code", [
+    (dict(sh=_sh(bt=3)), -2), (dict(sh=_sh(head_dim=96)), -2), (dict(sh=_sh(mode=5)), -1),
+    (dict(nr=_nr(dims=(3, 2, 2))), -2), (dict(nr=_nr(dims=(-2, 2, 2))), -2),
+    (dict(nr=_nr(dims=(64, 2, 0))), -2), (dict(nr=_nr(dims=(2 ** 31 - 2, 2 ** 31 - 2, 6))), -2),
+    (dict(nr=_nr(table=0)), -1), (dict(nr=_nr(table=0x100008)), -1),
+    (dict(nr=_nr(q=0x100004)), -1), (dict(nr=_nr(k=0x100004)), -1),
+    (dict(nr=_nr(eps=0.0)), -1), (dict(nr=_nr(eps=-1.0)), -1), (dict(nr=_nr(eps=float("nan"))), -1),
+    (dict(nr=_nr(eps=float("inf"))), -1),
+    (dict(q_in=None), -1), (dict(q_in=ODD), -1), (dict(ld=127), -1), (dict(ld=388), -1),
+    (dict(ld=0), -1), (dict(ld=1 << 50), -1),
+])
+def test_layer_calls_refuse(call, kw, code):
+    assert call(**kw) == code
+
+
+@pytest.mark.parametrize("kw", [dict(q=None), dict(q=ODD), dict(blocks=None), dict(blocks=ODD),
+                                dict(codes=OK), dict(scales=OK), dict(codes=ODD, scales=OK)])
+def test_forward_refuses(kw):
+    assert _fwd(**kw) == -1
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(dq=None), -1), (dict(dq=ODD), -1), (dict(out=None), -1), (dict(out=ODD), -1),
+    (dict(ld_out=64), -1), (dict(ld_out=130), -1), (dict(dw=ODD), -1), (dict(ws=None), -4),
+    (dict(ws=ODD), -4), (dict(n=1024), -4)])
+def test_backward_refuses(kw, code):
+    assert _bwd(**kw) == code
+
+
+def test_checkpoint_sources_refuse():
+    L = V.lib()
+    for codes, scales in ((None, OK), (OK, None), (ODD, OK), (OK, ODD)):
+        assert L.vmoba_qk_norm_rope_act8(_sh(), _nr(), codes, scales, OK, OK, OK, None) == -1
+        assert L.vmoba_qk_norm_rope_partition_act8(_sh(), _nr(), codes, scales, OK, OK, OK, OK,
+                                                   None) == -1
+        assert L.vmoba_qk_norm_rope_bwd_act8(_sh(), _nr(), codes, scales, OK, OK, OK, OK, OK, OK,
+                                             384, None, None, 0, None) == -1
+    assert L.vmoba_qk_norm_rope(_sh(), None, OK, OK, OK, 384, OK, OK, OK, None, None, None) == -1
+
+
+@pytest.mark.parametrize("args,code", [
+    (dict(dtype=2), -3), (dict(rows=-1), -2), (dict(cols=0), -2), (dict(ld=9), -2),
+    (dict(group=32), -2), (dict(group=0), -2), (dict(rows=1 << 40), -2),
+    (dict(rows=1 << 25, ld=1 << 39), -2), (dict(x=None), -1), (dict(codes=None), -1),
+    (dict(scales=None), -1), (dict(x=ctypes.c_void_p(0x100001)), -1),
+    (dict(scales=ctypes.c_void_p(0x100002)), -1), (dict(rows=0), 0)])
+def test_act8_refuses(args, code):
+    a = dict(dtype=0, x=OK, rows=4, cols=10, ld=10, group=64, codes=OK, scales=OK)
+    a.update(args)
+    L = V.lib()
+    assert L.vmoba_act8_pack(a["dtype"], a["x"], a["rows"], a["cols"], a["ld"], a["group"],
+                             a["codes"], a["scales"], None) == code
+    assert L.vmoba_act8_unpack(a["dtype"], a["codes"], a["scales"], a["rows"], a["cols"],
+                               a["group"], a["x"], a["ld"], None) == code
+
+
+@pytest.mark.parametrize("args,code", [
+    ((23, 20, 20, 1e4, 0, 0, 0, OK), -2), ((24, 20, 22, 1e4, 0, 0, 0, OK), -2),
+    ((24, 20, 20, 0.0, 0, 0, 0, OK), -1), ((24, 20, 20, float("nan"), 0, 0, 0, OK), -1),
+    ((24, 20, 20, float("inf"), 0, 0, 0, OK), -1), ((24, 20, 20, 1e4, 1 << 32, 0, 0, OK), -1),
+    ((24, 20, 20, 1e4, 0, 0, -(1 << 32), OK), -1), ((24, 20, 20, 1e4, 0, 0, 0, None), -1),
+    ((24, 20, 20, 1e4, 0, 0, 0, ODD), -1), ((0, 0, 0, 1e4, 0, 0, 0, None), 0)])
+def test_rope_table_refuses(args, code):
+    assert V.lib().vmoba_rope_table(_sh(), *args, None) == code
+
+
+def test_workspace_sizes():
+    for d in (64, 128):
+        n = V.qk_norm_rope_bwd_workspace_size(_shape(head_dim=d))
+        assert n >= 2 * d * 4 and n % 256 == 0
+    assert V.qk_norm_rope_bwd_workspace_size(_shape(bt=3)) == 0
+
+
+def test_binding_refuses_before_the_call():
+    sh = _shape()
+    s, h, d = sh.s, 2, 64
+    bf = torch.bfloat16
+    t = torch.zeros((s, h, d), dtype=bf)
+    qkv = torch.zeros((s, 3, h, d), dtype=bf)
+    nr = V.NormRope()
+    with pytest.raises(ValueError, match="CUDA"):
+        V.qk_norm_rope(sh, nr, qkv, t, t, t)
+    with pytest.raises(ValueError, match="shape"):
+        V.qk_norm_rope(sh, nr, qkv[1:], t, t, t)
+    with pytest.raises(ValueError, match="dtype"):
+        V.qk_norm_rope(sh, nr, qkv.float(), t, t, t)
+    with pytest.raises(ValueError, match="one tensor or three"):
+        V.qk_norm_rope(sh, nr, (t, t), t, t, t)
+    with pytest.raises(ValueError, match="checkpoint"):
+        c = V.Act8.empty((s, 3, h, d), d, "cpu")
+        V.qk_norm_rope(sh, nr, c, t, t, t, ckpt=c)
+    with pytest.raises(ValueError, match="groups of 64"):
+        V.qk_norm_rope(sh, nr, V.Act8.empty((s, 3, h, d), 128, "cpu"), t, t, t)
+    with pytest.raises(ValueError, match="64 or 128"):
+        V.Act8.empty((4, 4), 32, "cpu")
+    with pytest.raises(ValueError, match="bfloat16 or float32"):
+        V.act8_pack(torch.zeros((4, 4), dtype=torch.float16), V.Act8.empty((4, 4), 64, "cpu"))
+    with pytest.raises(ValueError, match="two axes"):
+        V.act8_pack(torch.zeros(4), V.Act8.empty((4,), 64, "cpu"))
+    with pytest.raises(ValueError, match="dense rows"):
+        V.act8_pack(torch.zeros((4, 8)).t(), V.Act8.empty((8, 4), 64, "cpu"))
+
+
+class _Fake:
+    """A stand-in with a CUDA tensor's attributes: what the layout checks read."""
+
+    def __init__(self, t, device="cuda:0"):
+        self.t, self.device = t, torch.device(device)
+        self.shape, self.dtype, self.is_cuda = t.shape, t.dtype, True
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
+def test_raw_rows_layouts():
+    sh = _shape()
+    s, h, d = sh.s, 2, 64
+    bf = torch.bfloat16
+
+    def raw(x):
+        return _lib._Call("x").raw(sh, x, bf, "qkv")
+
+    base = torch.zeros((s, 3 * h * d + 64), dtype=bf)
+    x = base.as_strided((s, 3, h, d), (base.stride(0), h * d, d, 1))
+    at, ld = raw(_Fake(x))
+    assert ld == 3 * h * d + 64 and [a - at[0] for a in at] == [0, 2 * h * d, 4 * h * d]
+    three = [torch.zeros((s, h, d), dtype=bf) for _ in range(3)]
+    at, ld = raw([_Fake(t) for t in three])
+    assert ld == h * d and at == [t.data_ptr() for t in three]
+    packed = torch.zeros((s, 3, h, d), dtype=bf)
+    at, ld = raw([_Fake(packed[:, i]) for i in range(3)])
+    assert ld == 3 * h * d
+    with pytest.raises(ValueError, match="one token stride"):
+        raw([_Fake(three[0]), _Fake(three[1]), _Fake(packed[:, 2])])
+    with pytest.raises(ValueError, match="overlap"):
+        raw(_Fake(packed[:1].expand(s, 3, h, d)))
+    with pytest.raises(ValueError, match="dense rows"):
+        raw(_Fake(torch.zeros((s, h, 3, d), dtype=bf).transpose(1, 2)))
+    with pytest.raises(ValueError, match="cuda:0"):
+        raw([_Fake(three[0]), _Fake(three[1], "cuda:1"), _Fake(three[2])])
+
+
+@pytest.mark.parametrize("kw,match", [
+    (dict(dims=(1, 2, 2)), "even"), (dict(dims=(64, 2, 0)), "even"), (dict(dims=(2, 2)), "even"),
+    (dict(dims=(2, 2, 2)), "rotation table"),
+    (dict(q_weight=torch.zeros(32)), "q_weight"), (dict(k_weight=torch.zeros(64)), "CUDA")])
+def test_norm_arguments_refused(kw, match):
+    with pytest.raises(ValueError, match=match):
+        _lib._Call("x").norm(_shape(), V.NormRope(**kw))
+
+
+def test_rope_dims():
+    assert V.rope_dims(128) == (44, 42, 42) and V.rope_dims(64) == (24, 20, 20)
+
+
+def test_plain_gradients_match_differences():
+    """The plain backward against central differences of the plain forward."""
+    rng = np.random.default_rng(3)
+    s, h, d = 6, 2, 8
+    z = R.phases(1, 2, 3, d, (2, 4, 2), R.table(1, 2, 3, (2, 4, 2)))
+    x, g, dy = rng.normal(size=(s, h, d)), rng.normal(size=d) + 1, rng.normal(size=(s, h, d))
+    dx, _, dg, _ = R.backward(x, g, 1e-3, z, dy)
+    step = 1e-5
+    for _ in range(8):
+        vx, vg = rng.normal(size=x.shape), rng.normal(size=d)
+        f = [(R.forward(x + e * vx, g + e * vg, 1e-3, z)[0] * dy).sum() for e in (step, -step)]
+        assert abs((f[0] - f[1]) / (2 * step) - (dx * vx).sum() - (dg * vg).sum()) < 1e-7
+
+
+def test_plain_rotation_is_the_stated_one():
+    """Brute force: each pair turned by its axis position's angle."""
+    T, H, W, d, dims, o = 2, 3, 4, 16, (4, 6, 2), (5, 0, 100)
+    z = R.phases(T, H, W, d, dims, R.table(T, H, W, dims, 100.0, o))
+    for t in range(T):
+        for y in range(H):
+            for x in range(W):
+                want = []
+                for pos, dim in zip((t + o[0], y + o[1], x + o[2]), dims):
+                    want += [pos * 100.0 ** (-2 * i / dim) for i in range(dim // 2)]
+                want += [0.0] * (d // 2 - len(want))
+                got = z[(t * H + y) * W + x]
+                assert np.allclose(got, np.exp(1j * np.array(want)), atol=1e-12)
