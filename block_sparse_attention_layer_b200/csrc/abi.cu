@@ -371,7 +371,7 @@ int norm_rope_fwd(const vmoba_shape* shape, const vmoba_norm_rope* nr, const voi
   if ((ckpt_codes || ckpt_scales) && !all_aligned({ckpt_codes, ckpt_scales})) return VMOBA_ERR_ARG;
   const NormRopeOut o{q, k, v, partition ? blocks : nullptr, ckpt_codes, ckpt_scales};
   drop_stale_error();
-  return cuda_status(launch_norm_rope(P, a, o, stream));
+  return cuda_status(launch_norm_rope(P, a, o, num_sms(), stream));
 }
 
 int norm_rope_bwd(const vmoba_shape* shape, const vmoba_norm_rope* nr, const void* q_in,

@@ -8,84 +8,153 @@
 // checkpoint.  A row's raw value is read once and its result written once:
 // HBM bound, 6 s n_h d elements.
 //
-// One CTA per (block, head); a warp holds R = 256 / d rows of that head, and
-// consecutive groups of R tokens go round the warps.  Token order is the case
-// of a single block that is the whole latent.
+// A CTA's eight warps take `hp` neighbouring heads; a warp holds R = 256 / d
+// rows of its head at a time and asks for the next ones before it works on
+// these.  A block of keys is cut into C chunks, one CTA each; the C CTAs are a
+// cluster, whose members add their column sums over distributed shared memory
+// in a fixed order.  Token order is the case of a single block that is the
+// whole latent, without clusters.
+#include <cooperative_groups.h>
+
 #include "rows.cuh"
 
 namespace vmoba {
 namespace {
 
 using namespace rows;
+namespace cg = cooperative_groups;
 
 constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kMaxHp = 4;
+constexpr int kFlush = 64;         // rows a lane adds in fp32 before they go to its fp64 sums
+
+// Where the rows of one launch lie.
+struct Walk {
+  int T, H, W, s, n_h;
+  int bt, bh, bw;                  // box of a block
+  int nbh, nbw, Nb, L;
+  FastDiv hw, w;                   // bh * bw, bw
+  int chunk, chunks;               // rows of a chunk, chunks of a block
+  int hp;                          // heads of a CTA
+  long long kv_tok, kv_head;       // strides of k and v by position and head
+};
+
+// One row of q, k and v as loaded.
+template <typename E, int D, bool From8>
+struct Rows {
+  Raw<E> q, k, v;
+  __device__ __forceinline__ void load(const NormRopeArgs& a, int n, int h, int n_h, int l) {
+    const long long at = n * a.ld + (long long)h * D;
+    q = load_row<D>(static_cast<const E*>(a.in[0]) + at, l);
+    k = load_row<D>(static_cast<const E*>(a.in[1]) + at, l);
+    v = load_row<D>(static_cast<const E*>(a.in[2]) + at, l);
+  }
+  __device__ __forceinline__ void values(float (&xq)[8], float (&xk)[8]) const {
+    unpack(q, xq);
+    unpack(k, xk);
+  }
+  __device__ __forceinline__ Raw<E> value() const { return v; }
+};
+template <typename E, int D>
+struct Rows<E, D, true> {
+  uint2 c[3];
+  float sc[3];
+  __device__ __forceinline__ void load(const NormRopeArgs& a, int n, int h, int n_h, int l) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const long long row = ((long long)n * 3 + i) * n_h + h;
+      c[i] = load_codes<E, D>(a.codes + row * D, l);
+      sc[i] = __ldg(a.scales + row);
+    }
+  }
+  __device__ __forceinline__ void values(float (&xq)[8], float (&xk)[8]) const {
+    decode8(c[0], sc[0], xq);
+    decode8(c[1], sc[1], xk);
+  }
+  __device__ __forceinline__ Raw<E> value() const {
+    float x[8];
+    decode8(c[2], sc[2], x);
+    Raw<E> r;
+    pack(x, r);
+    return r;
+  }
+};
 
 template <typename E, int D, bool From8, bool To8>
-__global__ void __launch_bounds__(kWarps * 32)
-k_norm_rope(Prob P, NormRopeArgs a, NormRopeOut o, int chunk, long long kv_tok,
-            long long kv_head) {
+__global__ void __launch_bounds__(kThreads, 2)
+k_norm_rope(Walk w, NormRopeArgs a, NormRopeOut o) {
   constexpr int G = D / 8, R = 32 / G;
-  __shared__ double red[kWarps * R][D];
+  __shared__ double sums[8][kThreads];       // a thread's fp64 column sums
+  __shared__ double total[kMaxHp * D];       // the CTA's, summed over the cluster at the end
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane / G, l = lane % G;
-  const int h = blockIdx.y;
-  // rows [first, last) of the partition order; a chunk never leaves its block
-  const int first = blockIdx.x * chunk, last = min(first + chunk, P.s);
+  const int h = blockIdx.y * w.hp + warp % w.hp;
+  const int j = blockIdx.x / w.chunks;
+  const int first = (blockIdx.x - j * w.chunks) * w.chunk, last = min(first + w.chunk, w.L);
+  const int step = kWarps / w.hp * R;
 
   float gq[8], gk[8];
   load_weights<E, D>(a.gq, l, gq);
   load_weights<E, D>(a.gk, l, gk);
-  const PairRefs refs = pair_refs<E, D>(l, P.T, P.H, a.ht, a.hh, a.hw);
-  const long long row3 = (long long)P.n_h * D;
-  double acc[8];
+  const PairRefs refs = pair_refs<E, D>(l, a.ht, a.hh, a.hw);
+  const int y_rows = w.T * a.ht, x_rows = y_rows + w.H * a.hh;
+  const long long row3 = (long long)w.n_h * D;
+  const int pw = j % w.nbw, jj = j / w.nbw, ph = jj % w.nbh, pt = jj / w.nbh;
+  const int t0 = pt * w.bt, y0 = ph * w.bh, x0 = pw * w.bw;
+  float acc[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i] = 0.0;
+  for (int i = 0; i < 8; ++i) {
+    acc[i] = 0.f;
+    sums[i][threadIdx.x] = 0.0;
+  }
 
-  for (int p0 = first + warp * R; p0 < last; p0 += kWarps * R) {
-    const bool mine = p0 + sub < last;
-    const int p = mine ? p0 + sub : last - 1;
-    const int n = perm_token(P, p);
-    const int t = n / (P.H * P.W), yx = n - t * (P.H * P.W), y = yx / P.W, x = yx - y * P.W;
-    float xq[8], xk[8], xv[8];
-    Raw<E> rv;
-    const long long ckpt = ((long long)n * 3 * P.n_h + h) * D;   // its q row; k, v: + row3, 2 row3
-    if constexpr (From8) {
-      float sc[3];
-      uint2 c[3];
-#pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        c[i] = load_codes<E, D>(a.codes + ckpt + i * row3, l);
-        sc[i] = __ldg(a.scales + ((long long)n * 3 + i) * P.n_h + h);
-      }
-      decode8(c[0], sc[0], xq);
-      decode8(c[1], sc[1], xk);
-      decode8(c[2], sc[2], xv);
-      pack(xv, rv);
-    } else {
-      const long long at = n * a.ld + (long long)h * D;
-      const Raw<E> rq = load_row<D>(static_cast<const E*>(a.in[0]) + at, l);
-      const Raw<E> rk = load_row<D>(static_cast<const E*>(a.in[1]) + at, l);
-      rv = load_row<D>(static_cast<const E*>(a.in[2]) + at, l);
-      unpack(rq, xq);
-      unpack(rk, xk);
+  // row r of the block is token n = (t, y, x)
+  int t, y, x, n;
+  auto locate = [&](int r) {
+    t = w.hw.div(r);
+    const int rest = r - t * (w.bh * w.bw);
+    y = w.w.div(rest);
+    x = x0 + rest - y * w.bw;
+    t += t0;
+    y += y0;
+    n = (t * w.H + y) * w.W + x;
+  };
+  Rows<E, D, From8> cur, next;
+  int r = first + warp / w.hp * R + sub;
+  if (r - sub < last) {
+    locate(min(r, last - 1));
+    cur.load(a, n, h, w.n_h, l);
+  }
+  int rows = 0;
+  for (; r - sub < last; r += step) {
+    const bool mine = r < last;
+    const int nn = n, rt = t * a.ht, ry = y_rows + y * a.hh, rx = x_rows + x * a.hw;
+    float2 cs[4];
+    load_turns(refs, a.table, rt, ry, rx, cs);
+    if (r - sub + step < last) {
+      locate(min(r + step, last - 1));
+      next.load(a, n, h, w.n_h, l);
     }
+    float xq[8], xk[8];
+    cur.values(xq, xk);
+    const Raw<E> rv = cur.value();
     if constexpr (To8) {
-      unpack(rv, xv);
-      float sc[3];
+      float sc[3], xv[8];
       uint2 c[3];
+      unpack(rv, xv);
       c[0] = encode8(xq, row_max<G>(abs_max_bits(xq)), sc[0]);
       c[1] = encode8(xk, row_max<G>(abs_max_bits(xk)), sc[1]);
       c[2] = encode8(xv, row_max<G>(abs_max_bits(xv)), sc[2]);
       if (mine) {
 #pragma unroll
         for (int i = 0; i < 3; ++i) {
-          store_codes<E, D>(o.codes + ckpt + i * row3, l, c[i]);
-          if (l == 0) o.scales[((long long)n * 3 + i) * P.n_h + h] = sc[i];
+          const long long row = ((long long)nn * 3 + i) * w.n_h + h;
+          store_codes<E, D>(o.codes + row * D, l, c[i]);
+          if (l == 0) o.scales[row] = sc[i];
         }
       }
     }
-    float2 cs[4];
-    load_turns(refs, a.table, t, y, x, cs);
     float pre;
     const float rq = inv_rms<D>(xq, a.eps, pre), rk = inv_rms<D>(xk, a.eps, pre);
 #pragma unroll
@@ -96,54 +165,107 @@ k_norm_rope(Prob P, NormRopeArgs a, NormRopeOut o, int chunk, long long kv_tok,
     turn(xq, cs);
     turn(xk, cs);
     if (mine) {
-      Raw<E> w;
-      pack(xq, w);
-      store_raw<D>(static_cast<E*>(o.q) + n * row3 + (long long)h * D, l, w);
-      pack(xk, w);
-      const long long at = p * kv_tok + h * kv_head;
-      store_raw<D>(static_cast<E*>(o.k) + at, l, w);
+      Raw<E> u;
+      pack(xq, u);
+      store_raw<D>(static_cast<E*>(o.q) + nn * row3 + (long long)h * D, l, u);
+      pack(xk, u);
+      const long long at = ((long long)j * w.L + r) * w.kv_tok + h * w.kv_head;
+      store_raw<D>(static_cast<E*>(o.k) + at, l, u);
       store_raw<D>(static_cast<E*>(o.v) + at, l, rv);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] += (double)xk[i];
+      for (int i = 0; i < 8; ++i) acc[i] += xk[i];
     }
+    if (++rows == kFlush) {
+      rows = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        sums[i][threadIdx.x] += (double)acc[i];
+        acc[i] = 0.f;
+      }
+    }
+    cur = next;
   }
   if (o.blocks == nullptr) return;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) red[warp * R + sub][elem_at<E, D>(l, i)] = acc[i];
+  for (int i = 0; i < 8; ++i) sums[i][threadIdx.x] += (double)acc[i];
   __syncthreads();
-  for (int c = threadIdx.x; c < D; c += blockDim.x) {
+  const int cols = w.hp * D;
+  for (int c = threadIdx.x; c < cols; c += kThreads) {
+    const int hh = c / D, i = c % D / G, ll = c % G;      // lanes apart: no bank conflicts
     double sum = 0.0;
-    for (int w = 0; w < kWarps * R; ++w) sum += red[w][c];
-    o.blocks[((size_t)h * P.Nb + blockIdx.x) * D + c] = (float)(sum / (double)P.L);
+    for (int v = hh; v < kWarps; v += w.hp)
+#pragma unroll
+      for (int b = 0; b < R; ++b) sum += sums[i][v * 32 + b * G + ll];
+    total[hh * D + elem_at<E, D>(ll, i)] = sum;
   }
+  cg::cluster_group cluster = cg::this_cluster();
+  cluster.sync();
+  const int rank = cluster.block_rank(), size = cluster.num_blocks();
+  for (int c = rank * kThreads + threadIdx.x; c < cols; c += size * kThreads) {
+    double sum = 0.0;
+    for (int m = 0; m < size; ++m) sum += cluster.map_shared_rank(total, m)[c];
+    o.blocks[((size_t)(blockIdx.y * w.hp + c / D) * w.Nb + j) * D + c % D] =
+        (float)(sum / (double)w.L);
+  }
+  cluster.sync();                    // a member's sums are read until here
 }
 
 template <typename E, int D, bool From8, bool To8>
-cudaError_t launch_t(Prob P, const NormRopeArgs& a, const NormRopeOut& o, cudaStream_t st) {
-  int chunk = P.L;
-  long long kv_tok = D, kv_head = (long long)P.s * D;
-  if (o.blocks == nullptr) {            // token order: one block that is the whole latent
-    P.bt = P.T; P.bh = P.H; P.bw = P.W;
-    P.nbt = P.nbh = P.nbw = P.Nb = 1;
-    P.L = P.s;
-    kv_tok = (long long)P.n_h * D;
-    kv_head = D;
-    chunk = 64;
+cudaError_t launch_t(const Prob& P, const NormRopeArgs& a, const NormRopeOut& o, int num_sms,
+                     cudaStream_t st) {
+  constexpr int R = 256 / D;
+  Walk w{};
+  w.T = P.T; w.H = P.H; w.W = P.W; w.s = P.s; w.n_h = P.n_h;
+  w.bt = P.bt; w.bh = P.bh; w.bw = P.bw;
+  w.nbh = P.nbh; w.nbw = P.nbw; w.Nb = P.Nb; w.L = P.L;
+  w.hp = P.n_h % 4 == 0 ? 4 : (P.n_h % 2 == 0 ? 2 : 1);
+  const int step = kWarps / w.hp * R, groups = P.n_h / w.hp;
+  if (o.blocks) {
+    w.kv_tok = D;
+    w.kv_head = (long long)P.s * D;
+    w.chunks = 1;
+    while (w.chunks < 8 && (long long)P.Nb * w.chunks * groups < 4 * num_sms &&
+           P.L > w.chunks * step * 2)
+      w.chunks *= 2;
+    w.chunk = (P.L + w.chunks - 1) / w.chunks;
+  } else {                             // token order: one block that is the whole latent
+    w.bt = P.T; w.bh = P.H; w.bw = P.W;
+    w.nbh = w.nbw = w.Nb = 1;
+    w.L = P.s;
+    w.kv_tok = (long long)P.n_h * D;
+    w.kv_head = D;
+    const long long want = 8LL * num_sms / groups + 1;
+    w.chunk = (int)((P.s + want - 1) / want);
+    w.chunk = (w.chunk + step - 1) / step * step;
+    w.chunks = (P.s + w.chunk - 1) / w.chunk;
   }
-  const dim3 grid((P.s + chunk - 1) / chunk, P.n_h);
+  w.hw = FastDiv(w.bh * w.bw);
+  w.w = FastDiv(w.bw);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(w.Nb * w.chunks, groups);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = o.blocks ? w.chunks : 1;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cudaError_t e;
   {
     VMOBA_TRACE("k_norm_rope", st);
-    k_norm_rope<E, D, From8, To8><<<grid, kWarps * 32, 0, st>>>(P, a, o, chunk, kv_tok, kv_head);
+    e = cudaLaunchKernelEx(&cfg, k_norm_rope<E, D, From8, To8>, w, a, o);
   }
   count_launches(1);
-  return cudaGetLastError();
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <typename E, int D>
-cudaError_t launch_d(const Prob& P, const NormRopeArgs& a, const NormRopeOut& o, cudaStream_t st) {
-  if (a.codes) return launch_t<E, D, true, false>(P, a, o, st);
-  if (o.codes) return launch_t<E, D, false, true>(P, a, o, st);
-  return launch_t<E, D, false, false>(P, a, o, st);
+cudaError_t launch_d(const Prob& P, const NormRopeArgs& a, const NormRopeOut& o, int num_sms,
+                     cudaStream_t st) {
+  if (a.codes) return launch_t<E, D, true, false>(P, a, o, num_sms, st);
+  if (o.codes) return launch_t<E, D, false, true>(P, a, o, num_sms, st);
+  return launch_t<E, D, false, false>(P, a, o, num_sms, st);
 }
 
 // (cos, sin) of every axis position and pair: the angle (origin + position) *
@@ -166,11 +288,12 @@ __global__ void k_rope_table(int T, int H, int W, int ht, int hh, int hw, double
 }  // namespace
 
 cudaError_t launch_norm_rope(const Prob& P, const NormRopeArgs& a, const NormRopeOut& o,
-                             cudaStream_t st) {
+                             int num_sms, cudaStream_t st) {
   if (P.dtype == VMOBA_BF16)
-    return P.d == 128 ? launch_d<__nv_bfloat16, 128>(P, a, o, st)
-                      : launch_d<__nv_bfloat16, 64>(P, a, o, st);
-  return P.d == 128 ? launch_d<float, 128>(P, a, o, st) : launch_d<float, 64>(P, a, o, st);
+    return P.d == 128 ? launch_d<__nv_bfloat16, 128>(P, a, o, num_sms, st)
+                      : launch_d<__nv_bfloat16, 64>(P, a, o, num_sms, st);
+  return P.d == 128 ? launch_d<float, 128>(P, a, o, num_sms, st)
+                    : launch_d<float, 64>(P, a, o, num_sms, st);
 }
 
 cudaError_t launch_rope_table(int T, int H, int W, int ht, int hh, int hw, double base,

@@ -35,7 +35,7 @@ k_norm_rope_bwd(Prob P, NormRopeArgs a, const E* __restrict__ dq, const E* __res
   float gq[8], gk[8];
   load_weights<E, D>(a.gq, l, gq);
   load_weights<E, D>(a.gk, l, gk);
-  const PairRefs refs = pair_refs<E, D>(l, P.T, P.H, a.ht, a.hh, a.hw);
+  const PairRefs refs = pair_refs<E, D>(l, a.ht, a.hh, a.hw);
   const long long row3 = (long long)P.n_h * D;
 #pragma unroll
   for (int i = 0; i < 16; ++i) sums[i][threadIdx.x] = 0.0;
@@ -65,7 +65,8 @@ k_norm_rope_bwd(Prob P, NormRopeArgs a, const E* __restrict__ dq, const E* __res
         unpack(load_row<D>(static_cast<const E*>(a.in[1]) + raw, l), xk);
       }
       float2 cs[4];
-      load_turns(refs, a.table, t, y, x, cs);
+      load_turns(refs, a.table, t * a.ht, P.T * a.ht + y * a.hh,
+                 P.T * a.ht + P.H * a.hh + x * a.hw, cs);
       const long long out = n * ld_out + (long long)h * D;
       if (mine) store_raw<D>(ov + out, l, uv);
 #pragma unroll

@@ -22,6 +22,24 @@ namespace rows {
 
 constexpr unsigned kAll = 0xFFFFFFFFu;
 
+// n / d for 0 <= n < 2^31 by a multiplication (round-up reciprocal in 33 bits).
+struct FastDiv {
+  uint32_t mul, shift;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t d) {
+    shift = 0;
+    while ((1u << shift) < d) ++shift;
+    mul = (uint32_t)((((1ull << shift) - d) << 32) / d + 1);
+  }
+  __host__ __device__ __forceinline__ int div(int n) const {
+#ifdef __CUDA_ARCH__
+    return (int)((__umulhi(mul, (uint32_t)n) + (uint32_t)n) >> shift);
+#else
+    return (int)(((uint32_t)(((uint64_t)mul * (uint32_t)n) >> 32) + (uint32_t)n) >> shift);
+#endif
+  }
+};
+
 template <typename E>
 struct Raw;  // a lane's eight elements as loaded
 template <>
@@ -36,14 +54,26 @@ __device__ __forceinline__ int elem_at(int l, int i) {
   return i < 4 ? l * 4 + i : D / 2 + l * 4 + i - 4;
 }
 
+// Rows pass once: they leave L1 to the rotation table and the weights.
+__device__ __forceinline__ uint4 load16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ float4 as_float4(const uint4& v) {
+  return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
+                     __uint_as_float(v.w));
+}
+
 template <int D>
 __device__ __forceinline__ Raw<__nv_bfloat16> load_row(const __nv_bfloat16* row, int l) {
-  return {__ldg(reinterpret_cast<const uint4*>(row) + l)};
+  return {load16(reinterpret_cast<const uint4*>(row) + l)};
 }
 template <int D>
 __device__ __forceinline__ Raw<float> load_row(const float* row, int l) {
   const float4* p = reinterpret_cast<const float4*>(row);
-  return {__ldg(p + l), __ldg(p + D / 8 + l)};
+  return {as_float4(load16(p + l)), as_float4(load16(p + D / 8 + l))};
 }
 
 template <int D>
@@ -203,38 +233,39 @@ __device__ __forceinline__ float inv_rms(float (&x)[8], float eps, float& pre) {
 
 // ---- rotation ----
 
-// The table entries that a lane's four pairs read: entry = base + stride *
-// position on the pair's axis (0, 1, 2 = t, y, x; 3 = the pair stays).
+// Where a lane's four pairs find their table entry: the pair's place in its
+// axis part and the axis (0, 1, 2 = t, y, x; 3 = the pair stays), two bits each.
 struct PairRefs {
-  int base[4], stride[4], axis[4];
+  int place[4];
+  uint32_t axes;
 };
 
 template <typename E, int D>
-__device__ __forceinline__ PairRefs pair_refs(int l, int T, int H, int ht, int hh, int hw) {
+__device__ __forceinline__ PairRefs pair_refs(int l, int ht, int hh, int hw) {
   PairRefs r;
+  r.axes = 0u;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     int p = elem_at<E, D>(l, 2 * i) / 2;
-    if (p < ht) {
-      r.axis[i] = 0; r.base[i] = p; r.stride[i] = ht;
-    } else if ((p -= ht) < hh) {
-      r.axis[i] = 1; r.base[i] = T * ht + p; r.stride[i] = hh;
-    } else if ((p -= hh) < hw) {
-      r.axis[i] = 2; r.base[i] = T * ht + H * hh + p; r.stride[i] = hw;
-    } else {
-      r.axis[i] = 3; r.base[i] = 0; r.stride[i] = 0;
-    }
+    uint32_t axis = 0u;
+    if (p >= ht) { p -= ht; axis = 1u; }
+    if (axis == 1u && p >= hh) { p -= hh; axis = 2u; }
+    if (axis == 2u && p >= hw) axis = 3u;
+    r.place[i] = p;
+    r.axes |= axis << (2 * i);
   }
   return r;
 }
 
-__device__ __forceinline__ void load_turns(const PairRefs& r, const float2* table, int t, int y,
-                                           int x, float2 (&cs)[4]) {
+// rt, ry, rx: the table rows of the token's t, y and x.
+__device__ __forceinline__ void load_turns(const PairRefs& r, const float2* table, int rt, int ry,
+                                           int rx, float2 (&cs)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int pos = r.axis[i] == 0 ? t : (r.axis[i] == 1 ? y : x);
+    const uint32_t axis = (r.axes >> (2 * i)) & 3u;
+    const int row = axis == 0u ? rt : (axis == 1u ? ry : rx);
     cs[i] = make_float2(1.f, 0.f);
-    if (r.axis[i] < 3) cs[i] = __ldg(table + r.base[i] + r.stride[i] * pos);
+    if (axis < 3u) cs[i] = __ldg(table + row + r.place[i]);
   }
 }
 
@@ -286,7 +317,7 @@ struct NormRopeOut {
 };
 
 cudaError_t launch_norm_rope(const Prob& P, const NormRopeArgs& a, const NormRopeOut& o,
-                             cudaStream_t st);
+                             int num_sms, cudaStream_t st);
 size_t norm_rope_bwd_ws_bytes(const Prob& P);
 cudaError_t launch_norm_rope_bwd(const Prob& P, const NormRopeArgs& a, const void* dq,
                                  const void* dk, const void* dv, void* const (&out)[3],
