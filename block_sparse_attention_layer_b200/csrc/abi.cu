@@ -326,7 +326,7 @@ bool all_aligned(std::initializer_list<const void*> ptrs) {
 // ld of raw rows: room for one kind's heads, 16-byte vectors.
 bool good_ld(const Prob& P, long long ld) {
   const int e = P.dtype == VMOBA_BF16 ? 2 : 4;
-  return ld >= (long long)P.n_h * P.d && ld <= (1LL << 40) && (ld * e) % 16 == 0;
+  return ld >= (long long)P.n_h * P.d && ld <= (1LL << 28) && (ld * e) % 16 == 0;
 }
 
 bool good_dims(const Prob& P, int dt, int dh, int dw) {

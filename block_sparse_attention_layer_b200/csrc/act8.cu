@@ -22,21 +22,20 @@ __device__ __forceinline__ void store1(__nv_bfloat16* p, float v) { *p = __float
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 
 // Eight neighbouring values.
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-  unpack(Raw<__nv_bfloat16>{__ldg(reinterpret_cast<const uint4*>(p))}, x);
+__device__ __forceinline__ Vals load8(const __nv_bfloat16* p) {
+  return unpack(Raw<__nv_bfloat16>{load16(p)});
 }
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4* q = reinterpret_cast<const float4*>(p);
-  unpack(Raw<float>{__ldg(q), __ldg(q + 1)}, x);
+__device__ __forceinline__ Vals load8(const float* p) {
+  return unpack(Raw<float>{as_float4(load16(p)), as_float4(load16(p + 4))});
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&x)[8]) {
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const Vals& v) {
   Raw<__nv_bfloat16> r;
-  pack(x, r);
+  pack(v, r);
   *reinterpret_cast<uint4*>(p) = r.u;
 }
-__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+__device__ __forceinline__ void store8(float* p, const Vals& v) {
   Raw<float> r;
-  pack(x, r);
+  pack(v, r);
   reinterpret_cast<float4*>(p)[0] = r.a;
   reinterpret_cast<float4*>(p)[1] = r.b;
 }
@@ -54,17 +53,17 @@ k_act8_pack(const E* __restrict__ x, long long n_groups, int per_row, int cols, 
   const int c0 = (int)(g - row * per_row) * Group;
   const E* src = x + row * ld;
   int8_t* dst = codes + row * cols;
-  float v[8];
+  Vals v;
   const int at = c0 + l * 8;
   if constexpr (Vec) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.f;
-    if (at < cols) load8(src + at, v);
+    for (int i = 0; i < 4; ++i) v.p[i] = both(0.f);
+    if (at < cols) v = load8(src + at);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int c = c0 + l + i * G;
-      v[i] = c < cols ? load1(src + c) : 0.f;
+      v.at(i) = c < cols ? load1(src + c) : 0.f;
     }
   }
   float scale;
@@ -97,10 +96,8 @@ k_act8_unpack(const int8_t* __restrict__ codes, const float* __restrict__ scales
   const float scale = __ldg(scales + g);
   if constexpr (Vec) {
     const int at = c0 + l * 8;
-    if (at >= cols) return;
-    float v[8];
-    decode8(__ldg(reinterpret_cast<const uint2*>(src + at)), scale, v);
-    store8(dst + at, v);
+    if (at < cols)
+      store8(dst + at, decode8(__ldg(reinterpret_cast<const uint2*>(src + at)), scale));
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {

@@ -8,12 +8,15 @@
 // checkpoint.  A row's raw value is read once and its result written once:
 // HBM bound, 6 s n_h d elements.
 //
-// A CTA's eight warps take `hp` neighbouring heads; a warp holds R = 256 / d
-// rows of its head at a time and asks for the next ones before it works on
-// these.  A block of keys is cut into C chunks, one CTA each; the C CTAs are a
-// cluster, whose members add their column sums over distributed shared memory
-// in a fixed order.  Token order is the case of a single block that is the
-// whole latent, without clusters.
+// A lane works on two rows of q, k and v at a time, two neighbouring heads of
+// one token where the head count is even (they share the position and its
+// table entries), else one head of two tokens: six loads in flight before the
+// first is used, and the four sums of squares go through one shuffle tree.  A
+// CTA's eight warps take `up` neighbouring units of heads, the rest of the
+// warps further tokens.  A block of keys is cut into chunks, one CTA each;
+// the CTAs of a block are a cluster, whose members add their column sums over
+// distributed shared memory in a fixed order.  Token order is the case of a
+// single block that is the whole latent, without clusters.
 #include <cooperative_groups.h>
 
 #include "rows.cuh"
@@ -26,176 +29,183 @@ namespace cg = cooperative_groups;
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kMaxHp = 4;
+constexpr int kMaxUp = 2;          // units of a CTA
 constexpr int kFlush = 64;         // rows a lane adds in fp32 before they go to its fp64 sums
 
 // Where the rows of one launch lie.
 struct Walk {
-  int T, H, W, s, n_h;
+  int T, H, W, n_h;
   int bt, bh, bw;                  // box of a block
   int nbh, nbw, Nb, L;
   FastDiv hw, w;                   // bh * bw, bw
   int chunk, chunks;               // rows of a chunk, chunks of a block
-  int hp;                          // heads of a CTA
-  long long kv_tok, kv_head;       // strides of k and v by position and head
+  int up;                          // units of heads of a CTA
+  uint32_t ld, kv_tok;             // bytes between tokens of the raw rows; positions of k and v
+  long long kv_head;               // elements between heads of k and v
 };
+
+template <typename T>
+__device__ __forceinline__ T* at_bytes(T* p, int n, uint32_t stride) {
+  return reinterpret_cast<T*>(
+      reinterpret_cast<uintptr_t>(p) + (unsigned long long)(uint32_t)n * stride);
+}
 
 // One row of q, k and v as loaded.
 template <typename E, int D, bool From8>
 struct Rows {
   Raw<E> q, k, v;
-  __device__ __forceinline__ void load(const NormRopeArgs& a, int n, int h, int n_h, int l) {
-    const long long at = n * a.ld + (long long)h * D;
-    q = load_row<D>(static_cast<const E*>(a.in[0]) + at, l);
-    k = load_row<D>(static_cast<const E*>(a.in[1]) + at, l);
-    v = load_row<D>(static_cast<const E*>(a.in[2]) + at, l);
+  __device__ __forceinline__ void load(const Walk& w, const NormRopeArgs& a, int n, int h, int l) {
+    q = load_row<D>(at_bytes(static_cast<const E*>(a.in[0]) + h * D, n, w.ld), l);
+    k = load_row<D>(at_bytes(static_cast<const E*>(a.in[1]) + h * D, n, w.ld), l);
+    v = load_row<D>(at_bytes(static_cast<const E*>(a.in[2]) + h * D, n, w.ld), l);
   }
-  __device__ __forceinline__ void values(float (&xq)[8], float (&xk)[8]) const {
-    unpack(q, xq);
-    unpack(k, xk);
-  }
+  __device__ __forceinline__ Vals query() const { return unpack(q); }
+  __device__ __forceinline__ Vals key() const { return unpack(k); }
   __device__ __forceinline__ Raw<E> value() const { return v; }
 };
 template <typename E, int D>
 struct Rows<E, D, true> {
   uint2 c[3];
   float sc[3];
-  __device__ __forceinline__ void load(const NormRopeArgs& a, int n, int h, int n_h, int l) {
+  __device__ __forceinline__ void load(const Walk& w, const NormRopeArgs& a, int n, int h, int l) {
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
-      const long long row = ((long long)n * 3 + i) * n_h + h;
-      c[i] = load_codes<E, D>(a.codes + row * D, l);
+      const uint32_t row = (uint32_t)((n * 3 + i) * w.n_h + h);
+      c[i] = load_codes<E, D>(at_bytes(a.codes, row, D), l);
       sc[i] = __ldg(a.scales + row);
     }
   }
-  __device__ __forceinline__ void values(float (&xq)[8], float (&xk)[8]) const {
-    decode8(c[0], sc[0], xq);
-    decode8(c[1], sc[1], xk);
-  }
+  __device__ __forceinline__ Vals query() const { return decode8(c[0], sc[0]); }
+  __device__ __forceinline__ Vals key() const { return decode8(c[1], sc[1]); }
   __device__ __forceinline__ Raw<E> value() const {
-    float x[8];
-    decode8(c[2], sc[2], x);
     Raw<E> r;
-    pack(x, r);
+    pack(decode8(c[2], sc[2]), r);
     return r;
   }
 };
 
-template <typename E, int D, bool From8, bool To8>
+template <typename E, int D, bool From8, bool To8, bool TwoHeads>
 __global__ void __launch_bounds__(kThreads, 2)
-k_norm_rope(Walk w, NormRopeArgs a, NormRopeOut o) {
-  constexpr int G = D / 8, R = 32 / G;
-  __shared__ double sums[8][kThreads];       // a thread's fp64 column sums
-  __shared__ double total[kMaxHp * D];       // the CTA's, summed over the cluster at the end
+k_norm_rope(const __grid_constant__ Walk w, const __grid_constant__ NormRopeArgs a,
+            const __grid_constant__ NormRopeOut o) {
+  constexpr int G = D / 8, R = 32 / G, NA = TwoHeads ? 2 : 1;
+  __shared__ double sums[NA][8][kThreads];       // a thread's fp64 column sums
+  __shared__ double total[kMaxUp * NA * D];      // the CTA's, summed over the cluster at the end
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane / G, l = lane % G;
-  const int h = blockIdx.y * w.hp + warp % w.hp;
+  const int h0 = (blockIdx.y * w.up + warp % w.up) * NA;
   const int j = blockIdx.x / w.chunks;
   const int first = (blockIdx.x - j * w.chunks) * w.chunk, last = min(first + w.chunk, w.L);
-  const int step = kWarps / w.hp * R;
+  const int step = kWarps / w.up * R;
 
-  float gq[8], gk[8];
-  load_weights<E, D>(a.gq, l, gq);
-  load_weights<E, D>(a.gk, l, gk);
+  const Vals gq = load_weights<E, D>(a.gq, l), gk = load_weights<E, D>(a.gk, l);
   const PairRefs refs = pair_refs<E, D>(l, a.ht, a.hh, a.hw);
   const int y_rows = w.T * a.ht, x_rows = y_rows + w.H * a.hh;
-  const long long row3 = (long long)w.n_h * D;
   const int pw = j % w.nbw, jj = j / w.nbw, ph = jj % w.nbh, pt = jj / w.nbh;
   const int t0 = pt * w.bt, y0 = ph * w.bh, x0 = pw * w.bw;
-  float acc[8];
+  Vals acc[NA];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    acc[i] = 0.f;
-    sums[i][threadIdx.x] = 0.0;
-  }
-
-  // row r of the block is token n = (t, y, x)
-  int t, y, x, n;
-  auto locate = [&](int r) {
-    t = w.hw.div(r);
-    const int rest = r - t * (w.bh * w.bw);
-    y = w.w.div(rest);
-    x = x0 + rest - y * w.bw;
-    t += t0;
-    y += y0;
-    n = (t * w.H + y) * w.W + x;
-  };
-  Rows<E, D, From8> cur, next;
-  int r = first + warp / w.hp * R + sub;
-  if (r - sub < last) {
-    locate(min(r, last - 1));
-    cur.load(a, n, h, w.n_h, l);
-  }
-  int rows = 0;
-  for (; r - sub < last; r += step) {
-    const bool mine = r < last;
-    const int nn = n, rt = t * a.ht, ry = y_rows + y * a.hh, rx = x_rows + x * a.hw;
-    float2 cs[4];
-    load_turns(refs, a.table, rt, ry, rx, cs);
-    if (r - sub + step < last) {
-      locate(min(r + step, last - 1));
-      next.load(a, n, h, w.n_h, l);
+  for (int u = 0; u < NA; ++u)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      acc[u].at(i) = 0.f;
+      sums[u][i][threadIdx.x] = 0.0;
     }
-    float xq[8], xk[8];
-    cur.values(xq, xk);
-    const Raw<E> rv = cur.value();
-    if constexpr (To8) {
-      float sc[3], xv[8];
-      uint2 c[3];
-      unpack(rv, xv);
-      c[0] = encode8(xq, row_max<G>(abs_max_bits(xq)), sc[0]);
-      c[1] = encode8(xk, row_max<G>(abs_max_bits(xk)), sc[1]);
-      c[2] = encode8(xv, row_max<G>(abs_max_bits(xv)), sc[2]);
-      if (mine) {
+
+  int rows = 0;
+  for (int r0 = first + warp / w.up * R; r0 < last; r0 += step * (TwoHeads ? 1 : 2)) {
+    int r[2], n[2];
+    bool mine[2];
+    Rows<E, D, From8> raw[2];
+    float2 cs[NA == 2 ? 1 : 2][4];
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
-          const long long row = ((long long)nn * 3 + i) * w.n_h + h;
-          store_codes<E, D>(o.codes + row * D, l, c[i]);
-          if (l == 0) o.scales[row] = sc[i];
+    for (int u = 0; u < 2; ++u) {
+      if (TwoHeads && u == 1) {
+        r[1] = r[0]; n[1] = n[0]; mine[1] = mine[0];
+      } else {
+        r[u] = r0 + u * step + sub;
+        mine[u] = r[u] < last;
+        // row r of the block is token n = (t, y, x)
+        const int rr = min(r[u], last - 1);
+        const int bt = w.hw.div(rr), rest = rr - bt * (w.bh * w.bw), by = w.w.div(rest);
+        const int t = t0 + bt, y = y0 + by, x = x0 + rest - by * w.bw;
+        n[u] = (t * w.H + y) * w.W + x;
+        load_turns(refs, a.table, t * a.ht, y_rows + y * a.hh, x_rows + x * a.hw, cs[u]);
+      }
+      raw[u].load(w, a, n[u], h0 + (TwoHeads ? u : 0), l);
+    }
+    Vals x[4] = {raw[0].query(), raw[0].key(), raw[1].query(), raw[1].key()};
+    if constexpr (To8) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const Vals v = unpack(raw[u].value());
+        float sc[3];
+        uint2 c[3];
+        c[0] = encode8(x[2 * u], row_max<G>(abs_max_bits(x[2 * u])), sc[0]);
+        c[1] = encode8(x[2 * u + 1], row_max<G>(abs_max_bits(x[2 * u + 1])), sc[1]);
+        c[2] = encode8(v, row_max<G>(abs_max_bits(v)), sc[2]);
+        if (mine[u]) {
+#pragma unroll
+          for (int i = 0; i < 3; ++i) {
+            const uint32_t row = (uint32_t)((n[u] * 3 + i) * w.n_h + h0 + (TwoHeads ? u : 0));
+            store_codes<E, D>(at_bytes(o.codes, row, D), l, c[i]);
+            if (l == 0) o.scales[row] = sc[i];
+          }
         }
       }
     }
-    float pre;
-    const float rq = inv_rms<D>(xq, a.eps, pre), rk = inv_rms<D>(xk, a.eps, pre);
+    float rms[4], pre[4];
+    inv_rms<D>(x, a.eps, l, rms, pre);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      xq[i] = xq[i] * rq * gq[i];
-      xk[i] = xk[i] * rk * gk[i];
-    }
-    turn(xq, cs);
-    turn(xk, cs);
-    if (mine) {
-      Raw<E> u;
-      pack(xq, u);
-      store_raw<D>(static_cast<E*>(o.q) + nn * row3 + (long long)h * D, l, u);
-      pack(xk, u);
-      const long long at = ((long long)j * w.L + r) * w.kv_tok + h * w.kv_head;
-      store_raw<D>(static_cast<E*>(o.k) + at, l, u);
-      store_raw<D>(static_cast<E*>(o.v) + at, l, rv);
+    for (int u = 0; u < 2; ++u) {
+      Vals &q = x[2 * u], &k = x[2 * u + 1];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] += xk[i];
-    }
-    if (++rows == kFlush) {
-      rows = 0;
+      for (int i = 0; i < 4; ++i) {
+        q.p[i] = __fmul2_rn(__fmul2_rn(q.p[i], both(rms[2 * u])), gq.p[i]);
+        k.p[i] = __fmul2_rn(__fmul2_rn(k.p[i], both(rms[2 * u + 1])), gk.p[i]);
+      }
+      turn(q, cs[TwoHeads ? 0 : u]);
+      turn(k, cs[TwoHeads ? 0 : u]);
+      if (mine[u]) {
+        const int h = h0 + (TwoHeads ? u : 0);
+        Raw<E> s;
+        pack(q, s);
+        store_raw<D>(at_bytes(static_cast<E*>(o.q) + h * D, n[u], w.n_h * D * sizeof(E)), l, s);
+        pack(k, s);
+        const int p = j * w.L + r[u];
+        store_raw<D>(at_bytes(static_cast<E*>(o.k) + h * w.kv_head, p, w.kv_tok), l, s);
+        store_raw<D>(at_bytes(static_cast<E*>(o.v) + h * w.kv_head, p, w.kv_tok), l,
+                     raw[u].value());
+        Vals& to = acc[TwoHeads ? u : 0];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        sums[i][threadIdx.x] += (double)acc[i];
-        acc[i] = 0.f;
+        for (int i = 0; i < 4; ++i) to.p[i] = __fadd2_rn(to.p[i], k.p[i]);
       }
     }
-    cur = next;
+    rows += TwoHeads ? 1 : 2;
+    if (rows >= kFlush) {
+      rows = 0;
+#pragma unroll
+      for (int u = 0; u < NA; ++u)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          sums[u][i][threadIdx.x] += (double)acc[u].at(i);
+          acc[u].at(i) = 0.f;
+        }
+    }
   }
   if (o.blocks == nullptr) return;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) sums[i][threadIdx.x] += (double)acc[i];
+  for (int u = 0; u < NA; ++u)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sums[u][i][threadIdx.x] += (double)acc[u].at(i);
   __syncthreads();
-  const int cols = w.hp * D;
+  const int cols = w.up * NA * D;
   for (int c = threadIdx.x; c < cols; c += kThreads) {
     const int hh = c / D, i = c % D / G, ll = c % G;      // lanes apart: no bank conflicts
     double sum = 0.0;
-    for (int v = hh; v < kWarps; v += w.hp)
+    for (int v = hh / NA; v < kWarps; v += w.up)
 #pragma unroll
-      for (int b = 0; b < R; ++b) sum += sums[i][v * 32 + b * G + ll];
+      for (int b = 0; b < R; ++b) sum += sums[hh % NA][i][v * 32 + b * G + ll];
     total[hh * D + elem_at<E, D>(ll, i)] = sum;
   }
   cg::cluster_group cluster = cg::this_cluster();
@@ -204,24 +214,26 @@ k_norm_rope(Walk w, NormRopeArgs a, NormRopeOut o) {
   for (int c = rank * kThreads + threadIdx.x; c < cols; c += size * kThreads) {
     double sum = 0.0;
     for (int m = 0; m < size; ++m) sum += cluster.map_shared_rank(total, m)[c];
-    o.blocks[((size_t)(blockIdx.y * w.hp + c / D) * w.Nb + j) * D + c % D] =
+    o.blocks[((size_t)(blockIdx.y * w.up * NA + c / D) * w.Nb + j) * D + c % D] =
         (float)(sum / (double)w.L);
   }
   cluster.sync();                    // a member's sums are read until here
 }
 
-template <typename E, int D, bool From8, bool To8>
+template <typename E, int D, bool From8, bool To8, bool TwoHeads>
 cudaError_t launch_t(const Prob& P, const NormRopeArgs& a, const NormRopeOut& o, int num_sms,
                      cudaStream_t st) {
   constexpr int R = 256 / D;
+  const int units = TwoHeads ? P.n_h / 2 : P.n_h;
   Walk w{};
-  w.T = P.T; w.H = P.H; w.W = P.W; w.s = P.s; w.n_h = P.n_h;
+  w.T = P.T; w.H = P.H; w.W = P.W; w.n_h = P.n_h;
   w.bt = P.bt; w.bh = P.bh; w.bw = P.bw;
   w.nbh = P.nbh; w.nbw = P.nbw; w.Nb = P.Nb; w.L = P.L;
-  w.hp = P.n_h % 4 == 0 ? 4 : (P.n_h % 2 == 0 ? 2 : 1);
-  const int step = kWarps / w.hp * R, groups = P.n_h / w.hp;
+  w.ld = (uint32_t)(a.ld * sizeof(E));
+  w.up = units % 2 == 0 ? 2 : 1;
+  const int step = kWarps / w.up * R, groups = units / w.up;
   if (o.blocks) {
-    w.kv_tok = D;
+    w.kv_tok = D * sizeof(E);
     w.kv_head = (long long)P.s * D;
     w.chunks = 1;
     while (w.chunks < 8 && (long long)P.Nb * w.chunks * groups < 4 * num_sms &&
@@ -232,7 +244,7 @@ cudaError_t launch_t(const Prob& P, const NormRopeArgs& a, const NormRopeOut& o,
     w.bt = P.T; w.bh = P.H; w.bw = P.W;
     w.nbh = w.nbw = w.Nb = 1;
     w.L = P.s;
-    w.kv_tok = (long long)P.n_h * D;
+    w.kv_tok = P.n_h * D * sizeof(E);
     w.kv_head = D;
     const long long want = 8LL * num_sms / groups + 1;
     w.chunk = (int)((P.s + want - 1) / want);
@@ -254,18 +266,25 @@ cudaError_t launch_t(const Prob& P, const NormRopeArgs& a, const NormRopeOut& o,
   cudaError_t e;
   {
     VMOBA_TRACE("k_norm_rope", st);
-    e = cudaLaunchKernelEx(&cfg, k_norm_rope<E, D, From8, To8>, w, a, o);
+    e = cudaLaunchKernelEx(&cfg, k_norm_rope<E, D, From8, To8, TwoHeads>, w, a, o);
   }
   count_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+template <typename E, int D, bool TwoHeads>
+cudaError_t launch_h(const Prob& P, const NormRopeArgs& a, const NormRopeOut& o, int num_sms,
+                     cudaStream_t st) {
+  if (a.codes) return launch_t<E, D, true, false, TwoHeads>(P, a, o, num_sms, st);
+  if (o.codes) return launch_t<E, D, false, true, TwoHeads>(P, a, o, num_sms, st);
+  return launch_t<E, D, false, false, TwoHeads>(P, a, o, num_sms, st);
+}
+
 template <typename E, int D>
 cudaError_t launch_d(const Prob& P, const NormRopeArgs& a, const NormRopeOut& o, int num_sms,
                      cudaStream_t st) {
-  if (a.codes) return launch_t<E, D, true, false>(P, a, o, num_sms, st);
-  if (o.codes) return launch_t<E, D, false, true>(P, a, o, num_sms, st);
-  return launch_t<E, D, false, false>(P, a, o, num_sms, st);
+  return P.n_h % 2 == 0 ? launch_h<E, D, true>(P, a, o, num_sms, st)
+                        : launch_h<E, D, false>(P, a, o, num_sms, st);
 }
 
 // (cos, sin) of every axis position and pair: the angle (origin + position) *

@@ -23,103 +23,137 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kChunk = 256;         // tokens of one work item
 constexpr int kMaxCtas = 1024;      // partial weight gradients in the workspace
 
-template <typename E, int D, bool From8>
-__global__ void __launch_bounds__(kThreads)
-k_norm_rope_bwd(Prob P, NormRopeArgs a, const E* __restrict__ dq, const E* __restrict__ dk,
-                const E* __restrict__ dv, E* oq, E* ok, E* ov, long long ld_out, float* part,
-                int n_items, int n_chunks) {
+template <typename T>
+__device__ __forceinline__ T* at_bytes(T* p, int n, uint32_t stride) {
+  return reinterpret_cast<T*>(
+      reinterpret_cast<uintptr_t>(p) + (unsigned long long)(uint32_t)n * stride);
+}
+
+struct Walk {
+  int T, H, W, s, n_h;
+  FastDiv hw, w;                   // H * W, W
+  uint32_t ld, ld_out;             // bytes between tokens
+  int n_items, n_chunks;
+};
+
+template <typename E, int D, bool From8, bool TwoHeads>
+__global__ void __launch_bounds__(kThreads, 2)
+k_norm_rope_bwd(const __grid_constant__ Walk w, const __grid_constant__ NormRopeArgs a,
+                const E* __restrict__ dq, const E* __restrict__ dk, const E* __restrict__ dv,
+                E* __restrict__ oq, E* __restrict__ ok, E* __restrict__ ov, float* part) {
   constexpr int G = D / 8, R = 32 / G;
   __shared__ double sums[16][kThreads];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane / G, l = lane % G;
-  float gq[8], gk[8];
-  load_weights<E, D>(a.gq, l, gq);
-  load_weights<E, D>(a.gk, l, gk);
+  const Vals gq = load_weights<E, D>(a.gq, l), gk = load_weights<E, D>(a.gk, l);
   const PairRefs refs = pair_refs<E, D>(l, a.ht, a.hh, a.hw);
-  const long long row3 = (long long)P.n_h * D;
+  const int y_rows = w.T * a.ht, x_rows = y_rows + w.H * a.hh;
+  const uint32_t row3 = w.n_h * D * sizeof(E);
 #pragma unroll
   for (int i = 0; i < 16; ++i) sums[i][threadIdx.x] = 0.0;
 
-  for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
-    const int h = item / n_chunks, c0 = (item - h * n_chunks) * kChunk;
-    const int last = min(c0 + kChunk, P.s);
-    float wq[8], wk[8];
+  for (int item = blockIdx.x; item < w.n_items; item += gridDim.x) {
+    const int unit = item / w.n_chunks, c0 = (item - unit * w.n_chunks) * kChunk;
+    const int h0 = unit * (TwoHeads ? 2 : 1);
+    const int last = min(c0 + kChunk, w.s);
+    Vals wq, wk;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) wq[i] = wk[i] = 0.f;
-    for (int n0 = c0 + warp * R; n0 < last; n0 += kWarps * R) {
-      const bool mine = n0 + sub < last;
-      const int n = mine ? n0 + sub : last - 1;
-      const int t = n / (P.H * P.W), yx = n - t * (P.H * P.W), y = yx / P.W, x = yx - y * P.W;
-      const long long at = n * row3 + (long long)h * D;
-      const Raw<E> uq = load_row<D>(dq + at, l), uk = load_row<D>(dk + at, l),
-                   uv = load_row<D>(dv + at, l);
-      float xq[8], xk[8];
-      if constexpr (From8) {
-        const long long ckpt = ((long long)n * 3 * P.n_h + h) * D;
-        const float* sc = a.scales + (long long)n * 3 * P.n_h + h;
-        decode8(load_codes<E, D>(a.codes + ckpt, l), __ldg(sc), xq);
-        decode8(load_codes<E, D>(a.codes + ckpt + row3, l), __ldg(sc + P.n_h), xk);
-      } else {
-        const long long raw = n * a.ld + (long long)h * D;
-        unpack(load_row<D>(static_cast<const E*>(a.in[0]) + raw, l), xq);
-        unpack(load_row<D>(static_cast<const E*>(a.in[1]) + raw, l), xk);
-      }
-      float2 cs[4];
-      load_turns(refs, a.table, t * a.ht, P.T * a.ht + y * a.hh,
-                 P.T * a.ht + P.H * a.hh + x * a.hw, cs);
-      const long long out = n * ld_out + (long long)h * D;
-      if (mine) store_raw<D>(ov + out, l, uv);
+    for (int i = 0; i < 4; ++i) wq.p[i] = wk.p[i] = both(0.f);
+    constexpr int kStep = kWarps * R;
+    for (int n0 = c0 + warp * R; n0 < last; n0 += kStep * (TwoHeads ? 1 : 2)) {
+      int n[2];
+      bool mine[2];
+      float2 cs[TwoHeads ? 1 : 2][4];
+      Raw<E> uq[2], uk[2], uv[2];
+      Vals x[4];
+      [[maybe_unused]] Raw<E> xq[2], xk[2];
+      [[maybe_unused]] uint2 cq[2], ck[2];
+      [[maybe_unused]] float sq[2], sk[2];
 #pragma unroll
-      for (int which = 0; which < 2; ++which) {
-        float(&xx)[8] = which ? xk : xq;
-        const float(&g)[8] = which ? gk : gq;
-        float(&wsum)[8] = which ? wk : wq;
-        float u[8];
-        unpack(which ? uk : uq, u);
-        turn_back(u, cs);
-        float pre;
-        const float r = inv_rms<D>(xx, a.eps, pre);
-        float dot = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          xx[i] *= r;                                // xh
-          if (mine) wsum[i] = fmaf(u[i], xx[i], wsum[i]);
-          u[i] *= g[i];
-          dot = fmaf(u[i], xx[i], dot);
+      for (int u = 0; u < 2; ++u) {
+        if (TwoHeads && u == 1) {
+          n[1] = n[0]; mine[1] = mine[0];
+        } else {
+          mine[u] = n0 + u * kStep + sub < last;
+          n[u] = min(n0 + u * kStep + sub, last - 1);
+          const int t = w.hw.div(n[u]), yx = n[u] - t * (w.H * w.W), y = w.w.div(yx);
+          load_turns(refs, a.table, t * a.ht, y_rows + y * a.hh, x_rows + (yx - y * w.W) * a.hw,
+                     cs[u]);
         }
-        dot = row_sum<G>(dot) * (1.0f / D);
-        const float rr = r * pre;
+        const int h = h0 + (TwoHeads ? u : 0);
+        uq[u] = load_row<D>(at_bytes(dq + h * D, n[u], row3), l);
+        uk[u] = load_row<D>(at_bytes(dk + h * D, n[u], row3), l);
+        uv[u] = load_row<D>(at_bytes(dv + h * D, n[u], row3), l);
+        if constexpr (From8) {
+          const uint32_t row = (uint32_t)(n[u] * 3 * w.n_h + h);
+          cq[u] = load_codes<E, D>(at_bytes(a.codes, row, D), l);
+          ck[u] = load_codes<E, D>(at_bytes(a.codes, row + w.n_h, D), l);
+          sq[u] = __ldg(a.scales + row);
+          sk[u] = __ldg(a.scales + row + w.n_h);
+        } else {
+          xq[u] = load_row<D>(at_bytes(static_cast<const E*>(a.in[0]) + h * D, n[u], w.ld), l);
+          xk[u] = load_row<D>(at_bytes(static_cast<const E*>(a.in[1]) + h * D, n[u], w.ld), l);
+        }
+      }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) u[i] = rr * fmaf(-xx[i], dot, u[i]);
-        if (mine) {
-          Raw<E> w;
-          pack(u, w);
-          store_raw<D>((which ? ok : oq) + out, l, w);
+      for (int u = 0; u < 2; ++u) {
+        if constexpr (From8) {
+          x[2 * u] = decode8(cq[u], sq[u]);
+          x[2 * u + 1] = decode8(ck[u], sk[u]);
+        } else {
+          x[2 * u] = unpack(xq[u]);
+          x[2 * u + 1] = unpack(xk[u]);
+        }
+        if (mine[u])
+          store_raw<D>(at_bytes(ov + (h0 + (TwoHeads ? u : 0)) * D, n[u], w.ld_out), l, uv[u]);
+      }
+      float r[4], pre[4], dot[4];
+      inv_rms<D>(x, a.eps, l, r, pre);
+      Vals g[4];                                // the gradients, then w = u g
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        g[k] = unpack(k & 1 ? uk[k / 2] : uq[k / 2]);
+        turn_back(g[k], cs[TwoHeads ? 0 : k / 2]);
+        Vals& sum = k & 1 ? wk : wq;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[k].p[i] = __fmul2_rn(x[k].p[i], both(r[k]));                // xh
+          if (mine[k / 2]) sum.p[i] = __ffma2_rn(g[k].p[i], x[k].p[i], sum.p[i]);
+          g[k].p[i] = __fmul2_rn(g[k].p[i], k & 1 ? gk.p[i] : gq.p[i]);
+        }
+        dot[k] = lane_dot(g[k], x[k]);
+      }
+      spread<G>(quarter_sums<G>(dot, l) * (-1.0f / D), dot);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float rr = r[k] * pre[k];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          g[k].p[i] = __fmul2_rn(__ffma2_rn(x[k].p[i], both(dot[k]), g[k].p[i]), both(rr));
+        if (mine[k / 2]) {
+          Raw<E> s;
+          pack(g[k], s);
+          const int h = h0 + (TwoHeads ? k / 2 : 0);
+          store_raw<D>(at_bytes((k & 1 ? ok : oq) + h * D, n[k / 2], w.ld_out), l, s);
         }
       }
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      sums[i][threadIdx.x] += (double)wq[i];
-      sums[8 + i][threadIdx.x] += (double)wk[i];
+      sums[i][threadIdx.x] += (double)wq.at(i);
+      sums[8 + i][threadIdx.x] += (double)wk.at(i);
     }
   }
   if (part == nullptr) return;
   __syncthreads();
-  // column c of the 2 D gradients: element i of lane l in every warp and row
+  // column e of the q and k gradients: element i of lane ll, over warps and rows
   for (int c = threadIdx.x; c < 2 * D; c += kThreads) {
-    const int e = c % D;
-    int ll, i;
-    if (sizeof(E) == 2) {
-      ll = e / 8; i = e % 8;
-    } else {
-      const int f = e % (D / 2);
-      ll = f / 4; i = f % 4 + (e >= D / 2 ? 4 : 0);
-    }
+    const int which = c / D, i = c % D / G, ll = c % G;
     double sum = 0.0;
-    for (int w = 0; w < kWarps; ++w)
-      for (int b = 0; b < R; ++b) sum += sums[i + (c >= D ? 8 : 0)][w * 32 + b * G + ll];
-    part[(size_t)blockIdx.x * 2 * D + c] = (float)sum;
+    for (int v = 0; v < kWarps; ++v)
+#pragma unroll
+      for (int b = 0; b < R; ++b) sum += sums[8 * which + i][v * 32 + b * G + ll];
+    part[(size_t)blockIdx.x * 2 * D + which * D + elem_at<E, D>(ll, i)] = (float)sum;
   }
 }
 
@@ -132,19 +166,25 @@ __global__ void k_norm_dweight(const float* __restrict__ part, int n, int cols,
   out[c] = (float)sum;
 }
 
-template <typename E, int D, bool From8>
+template <typename E, int D, bool From8, bool TwoHeads>
 cudaError_t launch_t(const Prob& P, const NormRopeArgs& a, const void* dq, const void* dk,
                      const void* dv, void* const (&out)[3], long long ld_out, float* dweight,
                      void* ws, int num_sms, cudaStream_t st) {
-  const int n_chunks = (P.s + kChunk - 1) / kChunk, n_items = n_chunks * P.n_h;
-  const int ctas = min(min(n_items, num_sms * 4), kMaxCtas);
+  Walk w{};
+  w.T = P.T; w.H = P.H; w.W = P.W; w.s = P.s; w.n_h = P.n_h;
+  w.hw = FastDiv(P.H * P.W);
+  w.w = FastDiv(P.W);
+  w.ld = (uint32_t)(a.ld * sizeof(E));
+  w.ld_out = (uint32_t)(ld_out * sizeof(E));
+  w.n_chunks = (P.s + kChunk - 1) / kChunk;
+  w.n_items = w.n_chunks * (TwoHeads ? P.n_h / 2 : P.n_h);
+  const int ctas = min(min(w.n_items, num_sms * 2), kMaxCtas);
   float* part = dweight ? static_cast<float*>(ws) : nullptr;
   {
     VMOBA_TRACE("k_norm_rope_bwd", st);
-    k_norm_rope_bwd<E, D, From8><<<ctas, kThreads, 0, st>>>(
-        P, a, static_cast<const E*>(dq), static_cast<const E*>(dk), static_cast<const E*>(dv),
-        static_cast<E*>(out[0]), static_cast<E*>(out[1]), static_cast<E*>(out[2]), ld_out, part,
-        n_items, n_chunks);
+    k_norm_rope_bwd<E, D, From8, TwoHeads><<<ctas, kThreads, 0, st>>>(
+        w, a, static_cast<const E*>(dq), static_cast<const E*>(dk), static_cast<const E*>(dv),
+        static_cast<E*>(out[0]), static_cast<E*>(out[1]), static_cast<E*>(out[2]), part);
   }
   count_launches(1);
   cudaError_t e = cudaGetLastError();
@@ -170,9 +210,12 @@ cudaError_t launch_norm_rope_bwd(const Prob& P, const NormRopeArgs& a, const voi
   auto go = [&](auto e, auto d) {
     using E = decltype(e);
     constexpr int D = decltype(d)::value;
-    return a.codes ? launch_t<E, D, true>(P, a, dq, dk, dv, out, ld_out, dweight, ws, num_sms, st)
-                   : launch_t<E, D, false>(P, a, dq, dk, dv, out, ld_out, dweight, ws, num_sms,
-                                           st);
+    auto call = [&](auto fn) {
+      return fn(P, a, dq, dk, dv, out, ld_out, dweight, ws, num_sms, st);
+    };
+    if (P.n_h % 2 == 0)
+      return a.codes ? call(launch_t<E, D, true, true>) : call(launch_t<E, D, false, true>);
+    return a.codes ? call(launch_t<E, D, true, false>) : call(launch_t<E, D, false, false>);
   };
   using D64 = std::integral_constant<int, 64>;
   using D128 = std::integral_constant<int, 128>;

@@ -87,34 +87,64 @@ __device__ __forceinline__ void store_raw(float* row, int l, const Raw<float>& r
   p[D / 8 + l] = r.b;
 }
 
-__device__ __forceinline__ void unpack(const Raw<__nv_bfloat16>& r, float (&x)[8]) {
+// A lane's eight values as four adjacent pairs: fp32 arithmetic runs on pairs
+// (two lanes of one instruction each), and a rotation turns one.
+struct Vals {
+  float2 p[4];
+  __device__ __forceinline__ float& at(int i) { return i & 1 ? p[i >> 1].y : p[i >> 1].x; }
+  __device__ __forceinline__ float at(int i) const { return i & 1 ? p[i >> 1].y : p[i >> 1].x; }
+};
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+__device__ __forceinline__ Vals unpack(const Raw<__nv_bfloat16>& r) {
   const uint32_t w[4] = {r.u.x, r.u.y, r.u.z, r.u.w};
+  Vals v;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
+  for (int i = 0; i < 4; ++i)
+    v.p[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+  return v;
 }
-__device__ __forceinline__ void unpack(const Raw<float>& r, float (&x)[8]) {
-  x[0] = r.a.x; x[1] = r.a.y; x[2] = r.a.z; x[3] = r.a.w;
-  x[4] = r.b.x; x[5] = r.b.y; x[6] = r.b.z; x[7] = r.b.w;
+__device__ __forceinline__ Vals unpack(const Raw<float>& r) {
+  return {make_float2(r.a.x, r.a.y), make_float2(r.a.z, r.a.w), make_float2(r.b.x, r.b.y),
+          make_float2(r.b.z, r.b.w)};
 }
 
 // The one rounding of a result: to the storage type, nearest even.
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
-  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<uint32_t*>(&v);
+__device__ __forceinline__ uint32_t bf16x2(float2 v) {
+  const __nv_bfloat162 w = __float22bfloat162_rn(v);
+  return *reinterpret_cast<const uint32_t*>(&w);
 }
-__device__ __forceinline__ void pack(const float (&x)[8], Raw<__nv_bfloat16>& r) {
-  r.u = make_uint4(bf16x2(x[0], x[1]), bf16x2(x[2], x[3]), bf16x2(x[4], x[5]),
-                   bf16x2(x[6], x[7]));
+__device__ __forceinline__ void pack(const Vals& v, Raw<__nv_bfloat16>& r) {
+  r.u = make_uint4(bf16x2(v.p[0]), bf16x2(v.p[1]), bf16x2(v.p[2]), bf16x2(v.p[3]));
 }
-__device__ __forceinline__ void pack(const float (&x)[8], Raw<float>& r) {
-  r.a = make_float4(x[0], x[1], x[2], x[3]);
-  r.b = make_float4(x[4], x[5], x[6], x[7]);
+__device__ __forceinline__ void pack(const Vals& v, Raw<float>& r) {
+  r.a = make_float4(v.p[0].x, v.p[0].y, v.p[1].x, v.p[1].y);
+  r.b = make_float4(v.p[2].x, v.p[2].y, v.p[3].x, v.p[3].y);
 }
 
-// Sum over the G lanes of a row (every lane of the warp takes part).
+// Four rows' sums over their G lanes at once (every lane of the warp takes
+// part).  Two exchange steps leave each lane with a quarter of one sum, the
+// rest of the tree adds those; nine shuffles instead of 4 log2 G.  The lane
+// that holds sum k is k * G / 4 of the group.
+template <int G>
+__device__ __forceinline__ float quarter_sums(const float (&v)[4], int l) {
+  const bool hi = l & (G / 2), hi2 = l & (G / 4);
+  float s0 = hi ? v[2] : v[0], s1 = hi ? v[3] : v[1];
+  s0 += __shfl_xor_sync(kAll, hi ? v[0] : v[2], G / 2);
+  s1 += __shfl_xor_sync(kAll, hi ? v[1] : v[3], G / 2);
+  float s = (hi2 ? s1 : s0) + __shfl_xor_sync(kAll, hi2 ? s0 : s1, G / 4);
+#pragma unroll
+  for (int o = G / 8; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
+  return s;
+}
+template <int G>
+__device__ __forceinline__ void spread(float s, float (&v)[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) v[k] = __shfl_sync(kAll, s, k * (G / 4), G);
+}
+
+// Sum over the G lanes of a row.
 template <int G>
 __device__ __forceinline__ float row_sum(float v) {
 #pragma unroll
@@ -128,14 +158,21 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v) {
   return v;
 }
 
+__device__ __forceinline__ float lane_dot(const Vals& a, const Vals& b) {
+  float2 s = __fmul2_rn(a.p[0], b.p[0]);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) s = __ffma2_rn(a.p[i], b.p[i], s);
+  return s.x + s.y;
+}
+
 // ---- 8-bit groups ----
 
 // The lane's part of max |x| as ordered bits (an infinity or NaN sorts above
 // every finite value).
-__device__ __forceinline__ uint32_t abs_max_bits(const float (&x)[8]) {
+__device__ __forceinline__ uint32_t abs_max_bits(const Vals& v) {
   uint32_t m = 0u;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v.at(i)) & 0x7FFFFFFFu);
   return m;
 }
 
@@ -146,7 +183,7 @@ __device__ __forceinline__ uint32_t abs_max_bits(const float (&x)[8]) {
 // border, where that error could decide, is redone in fp64 with a correctly
 // rounded division, whose quotient is exact enough for every bf16 and fp32
 // input to fall on the right side.
-__device__ __forceinline__ uint2 encode8(const float (&x)[8], uint32_t m, float& scale) {
+__device__ __forceinline__ uint2 encode8(const Vals& v, uint32_t m, float& scale) {
   const float a = __uint_as_float(m);
   if (m >= 0x7F800000u || a < 0x1p-119f) {
     scale = m >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : 0.f;
@@ -159,7 +196,7 @@ __device__ __forceinline__ uint2 encode8(const float (&x)[8], uint32_t m, float&
   float border = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float y = x[i] * inv;
+    const float y = v.at(i) * inv;
     const float z = y + kMagic;
     border = fmaxf(border, fabsf(y - (z - kMagic)));
     w[i] = __float_as_uint(z);
@@ -167,7 +204,7 @@ __device__ __forceinline__ uint2 encode8(const float (&x)[8], uint32_t m, float&
   if (border > 0.49998f) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      w[i] = (uint32_t)(int)rint((double)x[i] * 127.0 / (double)a);
+      w[i] = (uint32_t)(int)rint((double)v.at(i) * 127.0 / (double)a);
   }
   const uint32_t lo = __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040),
                                   0x5410);
@@ -178,12 +215,16 @@ __device__ __forceinline__ uint2 encode8(const float (&x)[8], uint32_t m, float&
 
 // code * scale of eight codes, exact integers times the fp32 scale (one
 // rounding).  A byte c + 128 in the mantissa of 2^23 is 2^23 + 128 + c.
-__device__ __forceinline__ void decode8(uint2 c, float scale, float (&x)[8]) {
+__device__ __forceinline__ Vals decode8(uint2 c, float scale) {
   const uint32_t w[2] = {c.x ^ 0x80808080u, c.y ^ 0x80808080u};
+  Vals v;
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    x[i] = (__uint_as_float(__byte_perm(w[i >> 2], 0x4B000000u, 0x7440 + (i & 3))) - 8388736.0f) *
-           scale;
+    v.at(i) = __uint_as_float(__byte_perm(w[i >> 2], 0x4B000000u, 0x7440 + (i & 3)));
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v.p[i] = __fmul2_rn(__fadd2_rn(v.p[i], both(-8388736.0f)), both(scale));
+  return v;
 }
 
 // A lane's eight codes of a row of D codes, in the element order of E.
@@ -206,29 +247,36 @@ __device__ __forceinline__ void store_codes(int8_t* row, int l, uint2 c) {
 
 // ---- norm ----
 
-// 1 / sqrt(mean x^2 + eps) of a row from the lane's eight elements.  Where
-// the squares leave fp32's range the row is first scaled by pre = 2^-80 (x
-// changes; eps then is far below the mean's last bit); else pre = 1.
+// r[k] = 1 / sqrt(mean x^2 + eps) of four rows.  Where a row's squares leave
+// fp32's range it is first scaled by pre[k] = 2^-80 (x changes; eps then is
+// far below the mean's last bit); else pre[k] = 1.
 template <int D>
-__device__ __forceinline__ float inv_rms(float (&x)[8], float eps, float& pre) {
+__device__ __forceinline__ void inv_rms(Vals (&x)[4], float eps, int l, float (&r)[4],
+                                        float (&pre)[4]) {
   constexpr int G = D / 8;
-  float ss = 0.f;
-  pre = 1.f;
+  float ss[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-  ss = row_sum<G>(ss);
-  const bool big = !(ss < 0x1p100f);
-  if (__any_sync(kAll, big)) {
-    float t = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (big) x[i] *= 0x1p-80f;
-      t = fmaf(x[i], x[i], t);
-    }
-    t = row_sum<G>(t);
-    if (big) { ss = t; eps = 0.f; pre = 0x1p-80f; }
+  for (int k = 0; k < 4; ++k) {
+    ss[k] = lane_dot(x[k], x[k]);
+    pre[k] = 1.f;
   }
-  return rsqrtf(fmaf(ss, 1.0f / D, eps));
+  const float s = quarter_sums<G>(ss, l);
+  spread<G>(rsqrtf(fmaf(s, 1.0f / D, eps)), r);
+  if (__any_sync(kAll, !(s < 0x1p100f))) {
+    float sum[4];
+    spread<G>(s, sum);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const bool big = !(sum[k] < 0x1p100f);
+      if (big) {
+        pre[k] = 0x1p-80f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[k].at(i) *= 0x1p-80f;
+      }
+      const float again = row_sum<G>(lane_dot(x[k], x[k]));
+      if (big) r[k] = rsqrtf(again * (1.0f / D));
+    }
+  }
 }
 
 // ---- rotation ----
@@ -270,29 +318,29 @@ __device__ __forceinline__ void load_turns(const PairRefs& r, const float2* tabl
 }
 
 // (y0, y1) -> (y0 c - y1 s, y0 s + y1 c)
-__device__ __forceinline__ void turn(float (&x)[8], const float2 (&cs)[4]) {
+__device__ __forceinline__ void turn(Vals& x, const float2 (&cs)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float a = x[2 * i], b = x[2 * i + 1];
-    x[2 * i] = fmaf(a, cs[i].x, -(b * cs[i].y));
-    x[2 * i + 1] = fmaf(a, cs[i].y, b * cs[i].x);
+    const float2 y = x.p[i], c = cs[i];
+    x.p[i] = make_float2(fmaf(y.x, c.x, -(y.y * c.y)), fmaf(y.x, c.y, y.y * c.x));
   }
 }
 // the transpose (= the inverse)
-__device__ __forceinline__ void turn_back(float (&x)[8], const float2 (&cs)[4]) {
+__device__ __forceinline__ void turn_back(Vals& x, const float2 (&cs)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float a = x[2 * i], b = x[2 * i + 1];
-    x[2 * i] = fmaf(a, cs[i].x, b * cs[i].y);
-    x[2 * i + 1] = fmaf(b, cs[i].x, -(a * cs[i].y));
+    const float2 y = x.p[i], c = cs[i];
+    x.p[i] = make_float2(fmaf(y.x, c.x, y.y * c.y), fmaf(y.y, c.x, -(y.x * c.y)));
   }
 }
 
 // A lane's eight weights of a row (ones where there are none).
 template <typename E, int D>
-__device__ __forceinline__ void load_weights(const float* g, int l, float (&w)[8]) {
+__device__ __forceinline__ Vals load_weights(const float* g, int l) {
+  Vals w;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = g ? __ldg(g + elem_at<E, D>(l, i)) : 1.f;
+  for (int i = 0; i < 8; ++i) w.at(i) = g ? __ldg(g + elem_at<E, D>(l, i)) : 1.f;
+  return w;
 }
 
 }  // namespace rows

@@ -327,7 +327,7 @@ int vmoba_score_select_static(const vmoba_shape* shape, const void* q, const flo
  * head_dim): the packed output of one projection ([s][3][n_heads][head_dim],
  * k = q + n_heads * head_dim, ld = 3 * n_heads * head_dim or more) or three
  * separate ones (ld = n_heads * head_dim).  Every pointer 16-byte aligned, ld
- * a multiple of 16 bytes.  Outputs must not overlap inputs. */
+ * a multiple of 16 bytes and at most 2^28.  Outputs must not overlap inputs. */
 typedef struct vmoba_norm_rope {
   const float* q_weight;      /* [head_dim] fp32 device, or NULL (all ones) */
   const float* k_weight;
