@@ -8,6 +8,7 @@ library is missing or fails to load, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from dataclasses import dataclass
@@ -72,6 +73,15 @@ class LayerShape:
     @property
     def s(self) -> int:
         return self.T * self.H * self.W
+
+    @functools.cached_property
+    def _ref(self):
+        """The shape as the ABI takes it, built once (the fields are frozen)."""
+        return ctypes.byref(self.c())
+
+    @functools.cached_property
+    def _blocks(self) -> int:
+        return num_blocks(self)
 
     def c(self) -> CShape:
         return CShape(self.T, self.H, self.W, self.n_heads, self.head_dim, self.mode,
@@ -364,21 +374,24 @@ class _Call:
     """Checks the tensors of one call and hands out their addresses: every one
     a CUDA tensor on the same device, which is current during the call."""
 
+    __slots__ = ("name", "device")
+
     def __init__(self, name: str):
         self.name = name
-        self.device = None
+        self.device = -2            # a host tensor's is -1
 
     def addr(self, t, shape, dtype, name, strided=False) -> int:
         if t.shape != shape:
             raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-        if t.dtype != dtype:
+        if t.dtype is not dtype:
             raise ValueError(f"{name}: expected dtype {dtype}, got {t.dtype}")
-        if not t.is_cuda:
-            raise ValueError(f"{name}: expected a CUDA tensor")
-        if self.device is None:
-            self.device = t.device
-        elif t.device != self.device:
-            raise ValueError(f"{name}: expected a tensor on {self.device}, got {t.device}")
+        device = t.get_device()
+        if device != self.device:
+            if not t.is_cuda:
+                raise ValueError(f"{name}: expected a CUDA tensor")
+            if self.device >= 0:
+                raise ValueError(f"{name}: expected a tensor on cuda:{self.device}, got {t.device}")
+            self.device = device
         if not strided and not t.is_contiguous():
             raise ValueError(f"{name}: expected a contiguous tensor")
         return t.data_ptr()
@@ -390,62 +403,74 @@ class _Call:
         if isinstance(x, (tuple, list)):
             if len(x) != 3:
                 raise ValueError(f"{name}: expected one tensor or three")
-            at = [self.addr(t, (s, h, d), dtype, name, strided=True) for t in x]
-            dense, tensors = (d, 1), x
-        else:
-            p = self.addr(x, (s, 3, h, d), dtype, name, strided=True)
-            at = [p + i * h * d * x.element_size() for i in range(3)]
-            dense, tensors = (h * d, d, 1), (x,)
-        ld = None
-        for t in tensors:
-            st = t.stride()
-            for n, have, want in zip(t.shape[1:], st[1:], dense):
-                if n > 1 and have != want:
-                    raise ValueError(f"{name}: expected dense rows, got strides {tuple(st)}")
-            if s > 1:
-                if ld is not None and st[0] != ld:
-                    raise ValueError(f"{name}: expected one token stride, got {ld} and {st[0]}")
-                ld = st[0]
-                if ld < (h * d if len(tensors) == 3 else 3 * h * d):
-                    raise ValueError(f"{name}: rows overlap, strides {tuple(st)}")
-        return at, (3 * h * d if ld is None else ld)
+            at = [self.addr(t, (s, h, d), dtype, name, True) for t in x]
+            ld = self.stride(x[0], h * d, (d, 1), name)
+            for t in x[1:]:
+                if self.stride(t, h * d, (d, 1), name) != ld:
+                    raise ValueError(f"{name}: expected one token stride, got "
+                                     f"{[t.stride(0) for t in x]}")
+            return at, ld
+        p, step = self.addr(x, (s, 3, h, d), dtype, name, True), h * d * x.element_size()
+        return (p, p + step, p + 2 * step), self.stride(x, 3 * h * d, (h * d, d, 1), name)
+
+    @staticmethod
+    def stride(t, least, dense, name) -> int:
+        """The token stride of rows whose other axes are dense."""
+        st = t.stride()
+        if st[1:] != dense and any(n > 1 and have != want
+                                   for n, have, want in zip(t.shape[1:], st[1:], dense)):
+            raise ValueError(f"{name}: expected dense rows, got strides {tuple(st)}")
+        if t.shape[0] == 1:
+            return least
+        if st[0] < least:
+            raise ValueError(f"{name}: rows overlap, strides {tuple(st)}")
+        return st[0]
 
     def norm(self, shape: LayerShape, nr: NormRope) -> CNormRope:
         import torch
-        dims = tuple(int(n) for n in nr.dims)
-        if len(dims) != 3 or min(dims) < 0 or any(n % 2 for n in dims) or \
-                sum(dims) > shape.head_dim:
+        try:
+            dt, dh, dw = nr.dims
+        except (TypeError, ValueError):
+            dt = dh = dw = -1
+        if dt < 0 or dh < 0 or dw < 0 or (dt | dh | dw) & 1 or dt + dh + dw > shape.head_dim:
             raise ValueError(f"dims: expected three even numbers >= 0 of sum <= "
                              f"{shape.head_dim}, got {nr.dims}")
-        g = [0 if w is None else self.addr(w, (shape.head_dim,), torch.float32, name)
-             for name, w in (("q_weight", nr.q_weight), ("k_weight", nr.k_weight))]
-        rows, table = _table_rows(shape, dims), 0
-        if rows:
+        gq, gk, table, d = nr.q_weight, nr.k_weight, 0, (shape.head_dim,)
+        if gq is not None:
+            gq = self.addr(gq, d, torch.float32, "q_weight")
+        if gk is not None:
+            gk = self.addr(gk, d, torch.float32, "k_weight")
+        if dt + dh + dw:
             if nr.table is None:
                 raise ValueError("table: expected a rotation table (rope_table)")
-            table = self.addr(nr.table, (rows, 2), torch.float32, "table")
-        return CNormRope(g[0], g[1], float(nr.eps), table, *dims)
+            table = self.addr(nr.table, (_table_rows(shape, nr.dims), 2), torch.float32, "table")
+        return CNormRope(gq, gk, nr.eps, table, dt, dh, dw)
 
     def ckpt(self, c: Act8, shape, group, name):
         import torch
         if c.group != group:
             raise ValueError(f"{name}: expected groups of {group}, got {c.group}")
         return (self.addr(c.codes, shape, torch.int8, name + ".codes"),
-                self.addr(c.scales, tuple(shape[:-1]) + (-(-shape[-1] // group),), torch.float32,
+                self.addr(c.scales, (*shape[:-1], -(-shape[-1] // group)), torch.float32,
                           name + ".scales"))
 
     def run(self, stream, *args) -> None:
         import torch
-        fn = getattr(lib(), self.name)
+        device = self.device
         if stream is None:
-            stream = torch.cuda.current_stream(self.device)
-        elif stream.device != self.device:
-            raise ValueError(f"stream: expected one of {self.device}, got {stream.device}")
-        if self.device.index == torch.cuda.current_device():
-            _check(self.name, fn(*args, stream.cuda_stream))
+            stream = torch._C._cuda_getCurrentRawStream(device)
+        elif stream.device.index != device:
+            raise ValueError(f"stream: expected one of cuda:{device}, got {stream.device}")
         else:
-            with torch.cuda.device(self.device):
-                _check(self.name, fn(*args, stream.cuda_stream))
+            stream = stream.cuda_stream
+        fn = getattr(_LIB or lib(), self.name)
+        if device == torch._C._cuda_getDevice():
+            rc = fn(*args, stream)
+        else:
+            with torch.cuda.device(device):
+                rc = fn(*args, stream)
+        if rc:
+            _check(self.name, rc)
 
 
 def rope_table(shape: LayerShape, dims, base: float = 10000.0, origin=(0, 0, 0), device="cuda",
@@ -458,7 +483,7 @@ def rope_table(shape: LayerShape, dims, base: float = 10000.0, origin=(0, 0, 0),
     table = torch.empty((max(_table_rows(shape, dims), 0), 2), dtype=torch.float32, device=device)
     c = _Call("vmoba_rope_table")
     at = c.addr(table, table.shape, torch.float32, "table")
-    c.run(stream, ctypes.byref(shape.c()), *dims, float(base), *(int(o) for o in origin), at)
+    c.run(stream, shape._ref, *dims, float(base), *(int(o) for o in origin), at)
     return table
 
 
@@ -477,7 +502,7 @@ def _norm_rope_fwd(name, shape, nr, qkv, outs, ckpt, stream):
         more = (0, 0) if ckpt is None else c.ckpt(ckpt, (s, 3, h, d), d, "ckpt")
     n = c.norm(shape, nr)
     out = [c.addr(t, sz, ty or dt, what) for t, sz, ty, what in outs]
-    c.run(stream, ctypes.byref(shape.c()), ctypes.byref(n), *src, *out, *more)
+    c.run(stream, shape._ref, ctypes.byref(n), *src, *out, *more)
 
 
 def qk_norm_rope(shape, nr, qkv, q, k, v, ckpt=None, stream=None):
@@ -501,11 +526,11 @@ def qk_norm_rope_partition(shape, nr, qkv, q, k_perm, v_perm, blocks, ckpt=None,
     _norm_rope_fwd("vmoba_qk_norm_rope_partition", shape, nr, qkv,
                    ((q, (s, h, d), None, "q"), (k_perm, (h, s, d), None, "k_perm"),
                     (v_perm, (h, s, d), None, "v_perm"),
-                    (blocks, (h, num_blocks(shape), d), torch.float32, "blocks")), ckpt, stream)
+                    (blocks, (h, shape._blocks, d), torch.float32, "blocks")), ckpt, stream)
 
 
 def qk_norm_rope_bwd_workspace_size(shape: LayerShape) -> int:
-    return lib().vmoba_qk_norm_rope_bwd_workspace_size(ctypes.byref(shape.c()))
+    return lib().vmoba_qk_norm_rope_bwd_workspace_size(shape._ref)
 
 
 def qk_norm_rope_bwd(shape, nr, qkv, dq, dk, dv, dqkv, dweight, ws, stream=None):
@@ -531,7 +556,7 @@ def qk_norm_rope_bwd(shape, nr, qkv, dq, dk, dv, dqkv, dweight, ws, stream=None)
         dw = c.addr(dweight, (2, full[2]), torch.float32, "dweight")
         n_ws = ws.numel() * ws.element_size()
         p_ws = c.addr(ws, ws.shape, ws.dtype, "ws")
-    c.run(stream, ctypes.byref(shape.c()), ctypes.byref(n), *src, *grads, *out, ld_out, dw, p_ws,
+    c.run(stream, shape._ref, ctypes.byref(n), *src, *grads, *out, ld_out, dw, p_ws,
           n_ws)
 
 

@@ -22,11 +22,9 @@ __device__ __forceinline__ void store1(__nv_bfloat16* p, float v) { *p = __float
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 
 // Eight neighbouring values.
-__device__ __forceinline__ Vals load8(const __nv_bfloat16* p) {
-  return unpack(Raw<__nv_bfloat16>{load16(p)});
-}
-__device__ __forceinline__ Vals load8(const float* p) {
-  return unpack(Raw<float>{as_float4(load16(p)), as_float4(load16(p + 4))});
+__device__ __forceinline__ Raw<__nv_bfloat16> load8(const __nv_bfloat16* p) { return {load16(p)}; }
+__device__ __forceinline__ Raw<float> load8(const float* p) {
+  return {as_float4(load16(p)), as_float4(load16(p + 4))};
 }
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const Vals& v) {
   Raw<__nv_bfloat16> r;
@@ -40,43 +38,81 @@ __device__ __forceinline__ void store8(float* p, const Vals& v) {
   reinterpret_cast<float4*>(p)[1] = r.b;
 }
 
+// Groups in order of rows.  A CTA takes kUnroll * kThreads / G of them in a
+// row; the 64-bit division that finds the first one's row is the CTA's, a
+// lane finds its own from there by a 32-bit multiplication.
+constexpr int kUnroll = 4;
+
+struct Shape {
+  long long n_groups, ld;
+  int per_row, cols;
+  FastDiv div;                     // per_row
+};
+
+struct Place {
+  long long row;
+  int c0;                          // first column
+};
+__device__ __forceinline__ Place place(const Shape& s, long long row0, int g0, int offset) {
+  const int g = g0 + offset, down = s.div.div(g);
+  return {row0 + down, g - down * s.per_row};
+}
+
 template <typename E, int Group, bool Vec>
 __global__ void __launch_bounds__(kThreads)
-k_act8_pack(const E* __restrict__ x, long long n_groups, int per_row, int cols, long long ld,
-            int8_t* __restrict__ codes, float* __restrict__ scales) {
-  constexpr int G = Group / 8;
+k_act8_pack(const E* __restrict__ x, const __grid_constant__ Shape s, int8_t* __restrict__ codes,
+            float* __restrict__ scales) {
+  constexpr int G = Group / 8, kPer = kThreads / G;
   const int l = threadIdx.x % G;
-  const long long g0 = ((long long)blockIdx.x * kThreads + threadIdx.x) / G;
-  const bool mine = g0 < n_groups;
-  const long long g = mine ? g0 : n_groups - 1;
-  const long long row = g / per_row;
-  const int c0 = (int)(g - row * per_row) * Group;
-  const E* src = x + row * ld;
-  int8_t* dst = codes + row * cols;
-  Vals v;
-  const int at = c0 + l * 8;
-  if constexpr (Vec) {
+  const long long base = (long long)blockIdx.x * (kUnroll * kPer);
+  const long long row0 = base / s.per_row;
+  const int g0 = (int)(base - row0 * s.per_row);
+  const int most = (int)min(s.n_groups - base, (long long)(kUnroll * kPer));
+  Raw<E> r[kUnroll];
+  Place at[kUnroll];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v.p[i] = both(0.f);
-    if (at < cols) v = load8(src + at);
-  } else {
+  for (int u = 0; u < kUnroll; ++u) {
+    const int k = u * kPer + threadIdx.x / G;
+    at[u] = place(s, row0, g0, min(k, most - 1));
+    at[u].c0 *= Group;
+    const E* src = x + at[u].row * s.ld;
+    if constexpr (Vec) {
+      const int c = at[u].c0 + l * 8;
+      Vals zero{};
+      pack(zero, r[u]);
+      if (c < s.cols) r[u] = load8(src + c);
+    } else {
+      Vals v;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = c0 + l + i * G;
-      v.at(i) = c < cols ? load1(src + c) : 0.f;
+      for (int i = 0; i < 8; ++i) {
+        const int c = at[u].c0 + l + i * G;
+        v.at(i) = c < s.cols ? load1(src + c) : 0.f;
+      }
+      pack(v, r[u]);               // exact: the values are the type's
     }
   }
-  float scale;
-  const uint2 w = encode8(v, row_max<G>(abs_max_bits(v)), scale);
-  if (!mine) return;
-  if (l == 0) scales[g] = scale;
-  if constexpr (Vec) {
-    if (at < cols) *reinterpret_cast<uint2*>(dst + at) = w;
-  } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = c0 + l + i * G;
-      if (c < cols) dst[c] = (int8_t)((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
+  for (int u = 0; u < kUnroll; u += 2) {
+    uint32_t m[2];
+    group_max<G>(r[u], r[u + 1], m[0], m[1]);
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int k = (u + b) * kPer + threadIdx.x / G;
+      if (k >= most) continue;
+      float scale;
+      const uint2 w = encode8(unpack(r[u + b]), m[b], scale);
+      if (l == 0) scales[base + k] = scale;
+      int8_t* dst = codes + at[u + b].row * s.cols;
+      if constexpr (Vec) {
+        const int c = at[u + b].c0 + l * 8;
+        if (c < s.cols) *reinterpret_cast<uint2*>(dst + c) = w;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int c = at[u + b].c0 + l + i * G;
+          if (c < s.cols) dst[c] = (int8_t)((i < 4 ? w.x : w.y) >> (8 * (i & 3)));
+        }
+      }
     }
   }
 }
@@ -84,47 +120,85 @@ k_act8_pack(const E* __restrict__ x, long long n_groups, int per_row, int cols, 
 template <typename E, int Group, bool Vec>
 __global__ void __launch_bounds__(kThreads)
 k_act8_unpack(const int8_t* __restrict__ codes, const float* __restrict__ scales,
-              long long n_groups, int per_row, int cols, E* __restrict__ out, long long ld) {
-  constexpr int G = Group / 8;
+              const __grid_constant__ Shape s, E* __restrict__ out) {
+  constexpr int G = Group / 8, kPer = kThreads / G;
   const int l = threadIdx.x % G;
-  const long long g = ((long long)blockIdx.x * kThreads + threadIdx.x) / G;
-  if (g >= n_groups) return;
-  const long long row = g / per_row;
-  const int c0 = (int)(g - row * per_row) * Group;
-  const int8_t* src = codes + row * cols;
-  E* dst = out + row * ld;
-  const float scale = __ldg(scales + g);
-  if constexpr (Vec) {
-    const int at = c0 + l * 8;
-    if (at < cols)
-      store8(dst + at, decode8(__ldg(reinterpret_cast<const uint2*>(src + at)), scale));
-  } else {
+  const long long base = (long long)blockIdx.x * (kUnroll * kPer);
+  const long long row0 = base / s.per_row;
+  const int g0 = (int)(base - row0 * s.per_row);
+  const int most = (int)min(s.n_groups - base, (long long)(kUnroll * kPer));
+  uint2 w[kUnroll];
+  float scale[kUnroll];
+  Place at[kUnroll];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = c0 + l + i * G;
-      if (c < cols) store1(dst + c, (float)src[c] * scale);
+  for (int u = 0; u < kUnroll; ++u) {
+    const int k = min(u * kPer + (int)threadIdx.x / G, most - 1);
+    at[u] = place(s, row0, g0, k);
+    at[u].c0 *= Group;
+    scale[u] = __ldg(scales + base + k);
+    const int8_t* src = codes + at[u].row * s.cols;
+    if constexpr (Vec) {
+      const int c = at[u].c0 + l * 8;
+      w[u] = make_uint2(0u, 0u);
+      if (c < s.cols) w[u] = __ldg(reinterpret_cast<const uint2*>(src + c));
+    } else {
+      uint32_t b[2] = {0u, 0u};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int c = at[u].c0 + l + i * G;
+        if (c < s.cols) b[i >> 2] |= (uint32_t)(uint8_t)src[c] << (8 * (i & 3));
+      }
+      w[u] = make_uint2(b[0], b[1]);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kUnroll; ++u) {
+    if (u * kPer + (int)threadIdx.x / G >= most) break;
+    const Vals v = decode8(w[u], scale[u]);
+    E* dst = out + at[u].row * s.ld;
+    if constexpr (Vec) {
+      const int c = at[u].c0 + l * 8;
+      if (c < s.cols) store8(dst + c, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int c = at[u].c0 + l + i * G;
+        if (c < s.cols) store1(dst + c, v.at(i));
+      }
     }
   }
 }
 
+template <int Group>
+Shape shape_of(long long n_rows, int cols, long long ld, unsigned* ctas) {
+  Shape s{};
+  s.per_row = (cols + Group - 1) / Group;
+  s.cols = cols;
+  s.ld = ld;
+  s.n_groups = n_rows * s.per_row;
+  s.div = FastDiv(s.per_row);
+  constexpr int per_cta = kUnroll * kThreads / (Group / 8);
+  *ctas = (unsigned)((s.n_groups + per_cta - 1) / per_cta);
+  return s;
+}
+
 bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+template <typename E>
+bool vectors(const void* x, long long ld, int cols, const int8_t* codes) {
+  return aligned(x, 16) && (ld * sizeof(E)) % 16 == 0 && cols % 8 == 0 && aligned(codes, 8);
+}
 
 template <typename E, int Group>
 cudaError_t pack_t(const void* x, long long n_rows, int cols, long long ld, int8_t* codes,
                    float* scales, cudaStream_t st) {
-  const int per_row = (cols + Group - 1) / Group;
-  const long long n = n_rows * per_row;
-  const long long ctas = (n * (Group / 8) + kThreads - 1) / kThreads;
-  const bool vec = aligned(x, 16) && (ld * sizeof(E)) % 16 == 0 && cols % 8 == 0 &&
-                   aligned(codes, 8);
+  unsigned ctas;
+  const Shape s = shape_of<Group>(n_rows, cols, ld, &ctas);
+  const auto kernel = vectors<E>(x, ld, cols, codes) ? k_act8_pack<E, Group, true>
+                                                     : k_act8_pack<E, Group, false>;
   {
     VMOBA_TRACE("k_act8_pack", st);
-    if (vec)
-      k_act8_pack<E, Group, true><<<(unsigned)ctas, kThreads, 0, st>>>(
-          static_cast<const E*>(x), n, per_row, cols, ld, codes, scales);
-    else
-      k_act8_pack<E, Group, false><<<(unsigned)ctas, kThreads, 0, st>>>(
-          static_cast<const E*>(x), n, per_row, cols, ld, codes, scales);
+    kernel<<<ctas, kThreads, 0, st>>>(static_cast<const E*>(x), s, codes, scales);
   }
   count_launches(1);
   return cudaGetLastError();
@@ -133,19 +207,13 @@ cudaError_t pack_t(const void* x, long long n_rows, int cols, long long ld, int8
 template <typename E, int Group>
 cudaError_t unpack_t(const int8_t* codes, const float* scales, long long n_rows, int cols,
                      void* out, long long ld, cudaStream_t st) {
-  const int per_row = (cols + Group - 1) / Group;
-  const long long n = n_rows * per_row;
-  const long long ctas = (n * (Group / 8) + kThreads - 1) / kThreads;
-  const bool vec = aligned(out, 16) && (ld * sizeof(E)) % 16 == 0 && cols % 8 == 0 &&
-                   aligned(codes, 8);
+  unsigned ctas;
+  const Shape s = shape_of<Group>(n_rows, cols, ld, &ctas);
+  const auto kernel = vectors<E>(out, ld, cols, codes) ? k_act8_unpack<E, Group, true>
+                                                       : k_act8_unpack<E, Group, false>;
   {
     VMOBA_TRACE("k_act8_unpack", st);
-    if (vec)
-      k_act8_unpack<E, Group, true><<<(unsigned)ctas, kThreads, 0, st>>>(
-          codes, scales, n, per_row, cols, static_cast<E*>(out), ld);
-    else
-      k_act8_unpack<E, Group, false><<<(unsigned)ctas, kThreads, 0, st>>>(
-          codes, scales, n, per_row, cols, static_cast<E*>(out), ld);
+    kernel<<<ctas, kThreads, 0, st>>>(codes, scales, s, static_cast<E*>(out));
   }
   count_launches(1);
   return cudaGetLastError();

@@ -44,53 +44,72 @@ struct Walk {
   long long kv_head;               // elements between heads of k and v
 };
 
-template <typename T>
-__device__ __forceinline__ T* at_bytes(T* p, int n, uint32_t stride) {
-  return reinterpret_cast<T*>(
-      reinterpret_cast<uintptr_t>(p) + (unsigned long long)(uint32_t)n * stride);
-}
-
-// One row of q, k and v as loaded.
+// One row of q, k and v on its way through shared memory.
 template <typename E, int D, bool From8>
-struct Rows {
-  Raw<E> q, k, v;
-  __device__ __forceinline__ void load(const Walk& w, const NormRopeArgs& a, int n, int h, int l) {
-    q = load_row<D>(at_bytes(static_cast<const E*>(a.in[0]) + h * D, n, w.ld), l);
-    k = load_row<D>(at_bytes(static_cast<const E*>(a.in[1]) + h * D, n, w.ld), l);
-    v = load_row<D>(at_bytes(static_cast<const E*>(a.in[2]) + h * D, n, w.ld), l);
+struct Feed {
+  static constexpr int kSlot = Slot<E, D>::kBytes, kBytes = 3 * kSlot;
+  __device__ __forceinline__ static void ask(char* s, const Walk& w, const NormRopeArgs& a, int n,
+                                             int h, int lane, int l) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      Slot<E, D>::ask(s + i * kSlot, at_bytes(static_cast<const E*>(a.in[i]) + h * D, n, w.ld),
+                      lane, l);
   }
-  __device__ __forceinline__ Vals query() const { return unpack(q); }
-  __device__ __forceinline__ Vals key() const { return unpack(k); }
-  __device__ __forceinline__ Raw<E> value() const { return v; }
+  __device__ __forceinline__ static Raw<E> raw(const char* s, int i, int lane) {
+    return Slot<E, D>::get(s + i * kSlot, lane);
+  }
+  __device__ __forceinline__ static Vals get(const char* s, int i, int lane) {
+    return unpack(raw(s, i, lane));
+  }
+  __device__ __forceinline__ static Raw<E> value(const char* s, int lane) {
+    return raw(s, 2, lane);
+  }
 };
 template <typename E, int D>
-struct Rows<E, D, true> {
-  uint2 c[3];
-  float sc[3];
-  __device__ __forceinline__ void load(const Walk& w, const NormRopeArgs& a, int n, int h, int l) {
+struct Feed<E, D, true> {
+  static constexpr int kSlot = Slot8<E, D>::kBytes, kBytes = 3 * kSlot;
+  __device__ __forceinline__ static void ask(char* s, const Walk& w, const NormRopeArgs& a, int n,
+                                             int h, int lane, int l) {
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
       const uint32_t row = (uint32_t)((n * 3 + i) * w.n_h + h);
-      c[i] = load_codes<E, D>(at_bytes(a.codes, row, D), l);
-      sc[i] = __ldg(a.scales + row);
+      Slot8<E, D>::ask(s + i * kSlot, at_bytes(a.codes, row, D), a.scales + row, lane, l);
     }
   }
-  __device__ __forceinline__ Vals query() const { return decode8(c[0], sc[0]); }
-  __device__ __forceinline__ Vals key() const { return decode8(c[1], sc[1]); }
-  __device__ __forceinline__ Raw<E> value() const {
+  __device__ __forceinline__ static Vals get(const char* s, int i, int lane) {
+    return decode8(Slot8<E, D>::codes(s + i * kSlot, lane), Slot8<E, D>::scale(s + i * kSlot, lane));
+  }
+  __device__ __forceinline__ static Raw<E> value(const char* s, int lane) {
     Raw<E> r;
-    pack(decode8(c[2], sc[2]), r);
+    pack(get(s, 2, lane), r);
     return r;
   }
 };
+
+// Iterations a warp's loads run ahead, and the CTAs of an SM that this leaves
+// shared memory for.
+template <typename E, bool From8>
+constexpr int stages() { return From8 || sizeof(E) == 2 ? 3 : 2; }
+
+template <typename E, int D, bool From8, bool TwoHeads>
+constexpr int smem_bytes() {
+  return stages<E, From8>() * kWarps * 2 * Feed<E, D, From8>::kBytes +
+         (TwoHeads ? 2 : 1) * (8 * kThreads + kMaxUp * D) * (int)sizeof(double);
+}
 
 template <typename E, int D, bool From8, bool To8, bool TwoHeads>
 __global__ void __launch_bounds__(kThreads, 2)
 k_norm_rope(const __grid_constant__ Walk w, const __grid_constant__ NormRopeArgs a,
             const __grid_constant__ NormRopeOut o) {
   constexpr int G = D / 8, R = 32 / G, NA = TwoHeads ? 2 : 1;
-  __shared__ double sums[NA][8][kThreads];       // a thread's fp64 column sums
-  __shared__ double total[kMaxUp * NA * D];      // the CTA's, summed over the cluster at the end
+  using F = Feed<E, D, From8>;
+  constexpr int S = stages<E, From8>();
+  extern __shared__ __align__(16) char smem[];
+  double(&sums)[NA][8][kThreads] =               // a thread's fp64 column sums
+      *reinterpret_cast<double(*)[NA][8][kThreads]>(smem);
+  double* total = &sums[0][0][0] + NA * 8 * kThreads;    // the CTA's, read by its cluster
+  char* ring = reinterpret_cast<char*>(total + kMaxUp * NA * D) +
+               (threadIdx.x >> 5) * (S * 2 * F::kBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane / G, l = lane % G;
   const int h0 = (blockIdx.y * w.up + warp % w.up) * NA;
@@ -112,12 +131,35 @@ k_norm_rope(const __grid_constant__ Walk w, const __grid_constant__ NormRopeArgs
       sums[u][i][threadIdx.x] = 0.0;
     }
 
-  int rows = 0;
-  for (int r0 = first + warp / w.up * R; r0 < last; r0 += step * (TwoHeads ? 1 : 2)) {
+  const int stride = step * (TwoHeads ? 1 : 2);
+  const int r_begin = first + warp / w.up * R;
+  // row r of the block is token n = (t, y, x)
+  auto locate = [&](int r, int& t, int& y, int& x) {
+    const int bt = w.hw.div(r), rest = r - bt * (w.bh * w.bw), by = w.w.div(rest);
+    t = t0 + bt;
+    y = y0 + by;
+    x = x0 + rest - by * w.bw;
+    return (t * w.H + y) * w.W + x;
+  };
+  auto ask = [&](int r0, int stage) {
+    if (r0 < last) {
+      int n = 0, t, y, x;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (!TwoHeads || u == 0) n = locate(min(r0 + u * step + sub, last - 1), t, y, x);
+        F::ask(ring + (stage * 2 + u) * F::kBytes, w, a, n, h0 + (TwoHeads ? u : 0), lane, l);
+      }
+    }
+    fetch_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) ask(r_begin + i * stride, i);
+  int rows = 0, stage = 0;
+  for (int r0 = r_begin; r0 < last; r0 += stride) {
+    ask(r0 + (S - 1) * stride, stage == 0 ? S - 1 : stage - 1);
     int r[2], n[2];
     bool mine[2];
-    Rows<E, D, From8> raw[2];
-    float2 cs[NA == 2 ? 1 : 2][4];
+    float2 cs[TwoHeads ? 1 : 2][4];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       if (TwoHeads && u == 1) {
@@ -125,31 +167,42 @@ k_norm_rope(const __grid_constant__ Walk w, const __grid_constant__ NormRopeArgs
       } else {
         r[u] = r0 + u * step + sub;
         mine[u] = r[u] < last;
-        // row r of the block is token n = (t, y, x)
-        const int rr = min(r[u], last - 1);
-        const int bt = w.hw.div(rr), rest = rr - bt * (w.bh * w.bw), by = w.w.div(rest);
-        const int t = t0 + bt, y = y0 + by, x = x0 + rest - by * w.bw;
-        n[u] = (t * w.H + y) * w.W + x;
+        int t, y, x;
+        n[u] = locate(min(r[u], last - 1), t, y, x);
         load_turns(refs, a.table, t * a.ht, y_rows + y * a.hh, x_rows + x * a.hw, cs[u]);
       }
-      raw[u].load(w, a, n[u], h0 + (TwoHeads ? u : 0), l);
     }
-    Vals x[4] = {raw[0].query(), raw[0].key(), raw[1].query(), raw[1].key()};
+    fetch_wait<S - 1>();
+    const char* in[2] = {ring + stage * 2 * F::kBytes, ring + (stage * 2 + 1) * F::kBytes};
+    stage = stage == S - 1 ? 0 : stage + 1;
+    Vals x[4] = {F::get(in[0], 0, lane), F::get(in[0], 1, lane), F::get(in[1], 0, lane),
+                 F::get(in[1], 1, lane)};
     if constexpr (To8) {
+      const Raw<E> raw[6] = {F::raw(in[0], 0, lane), F::raw(in[0], 1, lane),
+                             F::raw(in[0], 2, lane), F::raw(in[1], 0, lane),
+                             F::raw(in[1], 1, lane), F::raw(in[1], 2, lane)};
+      uint32_t m[6];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const Vals v = unpack(raw[u].value());
-        float sc[3];
-        uint2 c[3];
-        c[0] = encode8(x[2 * u], row_max<G>(abs_max_bits(x[2 * u])), sc[0]);
-        c[1] = encode8(x[2 * u + 1], row_max<G>(abs_max_bits(x[2 * u + 1])), sc[1]);
-        c[2] = encode8(v, row_max<G>(abs_max_bits(v)), sc[2]);
-        if (mine[u]) {
+      for (int i = 0; i < 3; ++i) group_max<G>(raw[i], raw[i + 3], m[i], m[i + 3]);
 #pragma unroll
-          for (int i = 0; i < 3; ++i) {
-            const uint32_t row = (uint32_t)((n[u] * 3 + i) * w.n_h + h0 + (TwoHeads ? u : 0));
-            store_codes<E, D>(at_bytes(o.codes, row, D), l, c[i]);
-            if (l == 0) o.scales[row] = sc[i];
+      for (int i = 0; i < 3; ++i) {
+        float sc[2];
+        uint2 c[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          c[u] = encode8(i < 2 ? x[2 * u + i] : unpack(raw[2 + 3 * u]), m[i + 3 * u], sc[u]);
+        const uint32_t row[2] = {(uint32_t)((n[0] * 3 + i) * w.n_h + h0),
+                                 (uint32_t)((n[1] * 3 + i) * w.n_h + h0 + (TwoHeads ? 1 : 0))};
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          if (mine[u]) store_codes<E, D>(at_bytes(o.codes, row[u], D), l, c[u]);
+        if (l == 0) {
+          if constexpr (TwoHeads) {      // an even row: two scales in one access
+            if (mine[0])
+              *reinterpret_cast<float2*>(o.scales + row[0]) = make_float2(sc[0], sc[1]);
+          } else {
+            if (mine[0]) o.scales[row[0]] = sc[0];
+            if (mine[1]) o.scales[row[1]] = sc[1];
           }
         }
       }
@@ -175,7 +228,7 @@ k_norm_rope(const __grid_constant__ Walk w, const __grid_constant__ NormRopeArgs
         const int p = j * w.L + r[u];
         store_raw<D>(at_bytes(static_cast<E*>(o.k) + h * w.kv_head, p, w.kv_tok), l, s);
         store_raw<D>(at_bytes(static_cast<E*>(o.v) + h * w.kv_head, p, w.kv_tok), l,
-                     raw[u].value());
+                     F::value(in[u], lane));
         Vals& to = acc[TwoHeads ? u : 0];
 #pragma unroll
         for (int i = 0; i < 4; ++i) to.p[i] = __fadd2_rn(to.p[i], k.p[i]);
@@ -235,10 +288,19 @@ cudaError_t launch_t(const Prob& P, const NormRopeArgs& a, const NormRopeOut& o,
   if (o.blocks) {
     w.kv_tok = D * sizeof(E);
     w.kv_head = (long long)P.s * D;
-    w.chunks = 1;
-    while (w.chunks < 8 && (long long)P.Nb * w.chunks * groups < 4 * num_sms &&
-           P.L > w.chunks * step * 2)
-      w.chunks *= 2;
+    // the chunk count whose CTAs, two on an SM at a time, get through the
+    // steps of the slowest slot first; each further CTA of a slot costs about
+    // two steps of filling and reducing
+    const int slots = 2 * num_sms;
+    long long best = -1;
+    for (int c = 1; c <= 8; ++c) {
+      const long long waves = ((long long)P.Nb * c * groups + slots - 1) / slots;
+      const long long cost = waves * (((P.L + c - 1) / c + step - 1) / step + 2);
+      if (best < 0 || cost < best) {
+        best = cost;
+        w.chunks = c;
+      }
+    }
     w.chunk = (P.L + w.chunks - 1) / w.chunks;
   } else {                             // token order: one block that is the whole latent
     w.bt = P.T; w.bh = P.H; w.bw = P.W;
@@ -256,6 +318,7 @@ cudaError_t launch_t(const Prob& P, const NormRopeArgs& a, const NormRopeOut& o,
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(w.Nb * w.chunks, groups);
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem_bytes<E, D, From8, TwoHeads>();
   cfg.stream = st;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -263,10 +326,13 @@ cudaError_t launch_t(const Prob& P, const NormRopeArgs& a, const NormRopeOut& o,
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  cudaError_t e;
+  const auto kernel = k_norm_rope<E, D, From8, To8, TwoHeads>;
+  static SmemOptIn opt_in;
+  cudaError_t e = opt_in.set(kernel, (int)cfg.dynamicSmemBytes);
+  if (e != cudaSuccess) return e;
   {
     VMOBA_TRACE("k_norm_rope", st);
-    e = cudaLaunchKernelEx(&cfg, k_norm_rope<E, D, From8, To8, TwoHeads>, w, a, o);
+    e = cudaLaunchKernelEx(&cfg, kernel, w, a, o);
   }
   count_launches(1);
   return e != cudaSuccess ? e : cudaGetLastError();

@@ -23,12 +23,6 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kChunk = 256;         // tokens of one work item
 constexpr int kMaxCtas = 1024;      // partial weight gradients in the workspace
 
-template <typename T>
-__device__ __forceinline__ T* at_bytes(T* p, int n, uint32_t stride) {
-  return reinterpret_cast<T*>(
-      reinterpret_cast<uintptr_t>(p) + (unsigned long long)(uint32_t)n * stride);
-}
-
 struct Walk {
   int T, H, W, s, n_h;
   FastDiv hw, w;                   // H * W, W
@@ -157,13 +151,22 @@ k_norm_rope_bwd(const __grid_constant__ Walk w, const __grid_constant__ NormRope
   }
 }
 
-__global__ void k_norm_dweight(const float* __restrict__ part, int n, int cols,
-                               float* __restrict__ out) {
-  const int c = blockIdx.x * blockDim.x + threadIdx.x;
-  if (c >= cols) return;
+// The CTAs' totals added up: 32 columns a block, 32 threads a column, each
+// over every 32nd CTA, and their sums in order.
+__global__ void __launch_bounds__(1024)
+k_norm_dweight(const float* __restrict__ part, int n, int cols, float* __restrict__ out) {
+  __shared__ double sums[32][33];
+  const int c = threadIdx.x & 31, k = threadIdx.x >> 5;
+  const float* p = part + blockIdx.x * 32 + c;
   double sum = 0.0;
-  for (int i = 0; i < n; ++i) sum += (double)part[(size_t)i * cols + c];
-  out[c] = (float)sum;
+#pragma unroll 8
+  for (int i = k; i < n; i += 32) sum += (double)__ldg(p + (size_t)i * cols);
+  sums[k][c] = sum;
+  __syncthreads();
+  if (k == 0) {
+    for (int i = 1; i < 32; ++i) sum += sums[i][c];
+    out[blockIdx.x * 32 + c] = (float)sum;
+  }
 }
 
 template <typename E, int D, bool From8, bool TwoHeads>
@@ -191,7 +194,7 @@ cudaError_t launch_t(const Prob& P, const NormRopeArgs& a, const void* dq, const
   if (e != cudaSuccess || !dweight) return e;
   {
     VMOBA_TRACE("k_norm_dweight", st);
-    k_norm_dweight<<<(2 * D + 31) / 32, 32, 0, st>>>(part, ctas, 2 * D, dweight);
+    k_norm_dweight<<<2 * D / 32, 1024, 0, st>>>(part, ctas, 2 * D, dweight);
   }
   count_launches(1);
   return cudaGetLastError();

@@ -15,6 +15,8 @@
 // stored as zeros.
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace vmoba {
@@ -75,6 +77,73 @@ __device__ __forceinline__ Raw<float> load_row(const float* row, int l) {
   const float4* p = reinterpret_cast<const float4*>(row);
   return {as_float4(load16(p + l)), as_float4(load16(p + D / 8 + l))};
 }
+
+// Asynchronous copies of a lane's own values into its own place in shared
+// memory: only the lane that asked for them reads them, so its own wait is the
+// only one needed, and loads stay in flight without holding registers.
+template <int Bytes>
+__device__ __forceinline__ void fetch(void* to, const void* from) {
+  const uint32_t dst = (uint32_t)__cvta_generic_to_shared(to);
+  if constexpr (Bytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(from) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" :: "r"(dst), "l"(from), "n"(Bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void fetch_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>  // at most the N newest groups still in flight
+__device__ __forceinline__ void fetch_wait() {
+  asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory");
+}
+
+template <typename T>
+__device__ __forceinline__ T* at_bytes(T* p, int n, uint32_t stride) {
+  return reinterpret_cast<T*>(
+      reinterpret_cast<uintptr_t>(p) + (unsigned long long)(uint32_t)n * stride);
+}
+
+// A warp's place for one access of its R rows, in the order of the lanes.
+template <typename E, int D>
+struct Slot {
+  static constexpr int kBytes = 32 * sizeof(Raw<E>);
+  __device__ __forceinline__ static void ask(char* s, const E* row, int lane, int l) {
+    fetch<16>(s + lane * 16, reinterpret_cast<const char*>(row) + l * 16);
+    if constexpr (sizeof(E) == 4)
+      fetch<16>(s + 512 + lane * 16, reinterpret_cast<const char*>(row) + D * 2 + l * 16);
+  }
+  __device__ __forceinline__ static Raw<E> get(const char* s, int lane) {
+    Raw<E> r;
+    if constexpr (sizeof(E) == 2) {
+      r.u = *reinterpret_cast<const uint4*>(s + lane * 16);
+    } else {
+      r.a = *reinterpret_cast<const float4*>(s + lane * 16);
+      r.b = *reinterpret_cast<const float4*>(s + 512 + lane * 16);
+    }
+    return r;
+  }
+};
+
+// The same for rows of codes with their scale.
+template <typename E, int D>
+struct Slot8 {
+  static constexpr int kBytes = 32 * 12;
+  __device__ __forceinline__ static void ask(char* s, const int8_t* codes, const float* scale,
+                                             int lane, int l) {
+    if constexpr (sizeof(E) == 2) {
+      fetch<8>(s + lane * 8, codes + l * 8);
+    } else {
+      fetch<4>(s + lane * 8, codes + l * 4);
+      fetch<4>(s + lane * 8 + 4, codes + D / 2 + l * 4);
+    }
+    fetch<4>(s + 256 + lane * 4, scale);
+  }
+  __device__ __forceinline__ static uint2 codes(const char* s, int lane) {
+    return *reinterpret_cast<const uint2*>(s + lane * 8);
+  }
+  __device__ __forceinline__ static float scale(const char* s, int lane) {
+    return *reinterpret_cast<const float*>(s + 256 + lane * 4);
+  }
+};
 
 template <int D>
 __device__ __forceinline__ void store_raw(__nv_bfloat16* row, int l, const Raw<__nv_bfloat16>& r) {
@@ -167,22 +236,56 @@ __device__ __forceinline__ float lane_dot(const Vals& a, const Vals& b) {
 
 // ---- 8-bit groups ----
 
-// The lane's part of max |x| as ordered bits (an infinity or NaN sorts above
-// every finite value).
-__device__ __forceinline__ uint32_t abs_max_bits(const Vals& v) {
+// Group maxima of |x| as bits: an infinity or NaN sorts above every finite
+// value.  bf16 works on the stored 16 bits, two values an instruction, and
+// two groups share the words of one shuffle tree.
+__device__ __forceinline__ uint32_t lane_max(const Raw<__nv_bfloat16>& r) {
+  constexpr uint32_t kAbs = 0x7FFF7FFFu;
+  return __vmaxu2(__vmaxu2(r.u.x & kAbs, r.u.y & kAbs), __vmaxu2(r.u.z & kAbs, r.u.w & kAbs));
+}
+template <int G>
+__device__ __forceinline__ void group_max(const Raw<__nv_bfloat16>& a,
+                                          const Raw<__nv_bfloat16>& b, uint32_t& ma,
+                                          uint32_t& mb) {
+  const uint32_t wa = lane_max(a), wb = lane_max(b);
+  uint32_t m = __vmaxu2(__byte_perm(wa, wb, 0x5410), __byte_perm(wa, wb, 0x7632));
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(kAll, m, o));
+  ma = m << 16;
+  mb = m & 0xFFFF0000u;
+}
+__device__ __forceinline__ uint32_t lane_max(const Raw<float>& r) {
+  const Vals v = unpack(r);
   uint32_t m = 0u;
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v.at(i)) & 0x7FFFFFFFu);
   return m;
 }
+template <int G>
+__device__ __forceinline__ void group_max(const Raw<float>& a, const Raw<float>& b, uint32_t& ma,
+                                          uint32_t& mb) {
+  ma = row_max<G>(lane_max(a));
+  mb = row_max<G>(lane_max(b));
+}
+
+// The code of one value for which the fp32 quotient cannot decide: rounds by
+// the sign of 127 x - T a, T the half integer next to c.  Both products are
+// taken with their rounding errors (an fma gives each exactly) and subtracted
+// leading parts first, so the sign is the exact one; zero is a tie, which
+// goes to the even code.
+__device__ __forceinline__ float settle(float x, float a, float c, float d) {
+  const float T = c + copysignf(0.5f, d);
+  const float q = 127.0f * x, p = T * a;
+  const float s = (q - p) + (fmaf(127.0f, x, -q) - fmaf(T, a, -p));
+  return s > 0.f ? T + 0.5f : (s < 0.f ? T - 0.5f : 2.0f * rintf(0.5f * T));
+}
 
 // Codes of a lane's eight values, byte i = element i, for a group whose
 // max |x| has the bits `m`; scale gets the group's.  The quotient is taken
-// as x * (127 / a) in fp32 (within 2^-16 absolute of the exact one) and
-// rounded by adding 1.5 * 2^23; a value that lands within 2e-5 of a rounding
-// border, where that error could decide, is redone in fp64 with a correctly
-// rounded division, whose quotient is exact enough for every bf16 and fp32
-// input to fall on the right side.
+// as x * (127 / a) in fp32, off by less than 2^-14 (reciprocal, two products:
+// 4 * 2^-24 relative of at most 127), and rounded by adding 1.5 * 2^23; where
+// one lands that close to a rounding border the lane settles its eight
+// exactly.
 __device__ __forceinline__ uint2 encode8(const Vals& v, uint32_t m, float& scale) {
   const float a = __uint_as_float(m);
   if (m >= 0x7F800000u || a < 0x1p-119f) {
@@ -190,22 +293,31 @@ __device__ __forceinline__ uint2 encode8(const Vals& v, uint32_t m, float& scale
     return make_uint2(0u, 0u);
   }
   scale = a / 127.0f;
-  const float inv = 127.0f / a;
+  // 127 a stays finite, and its reciprocal normal, with a large a scaled down
+  const float down = a > 0x1p100f ? 0x1p-8f : 1.0f;
+  float inv;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(a * down));
+  inv = inv * 127.0f * down;
   constexpr float kMagic = 12582912.0f;
   uint32_t w[8];
   float border = 0.f;
+  Vals y, z;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float y = v.at(i) * inv;
-    const float z = y + kMagic;
-    border = fmaxf(border, fabsf(y - (z - kMagic)));
-    w[i] = __float_as_uint(z);
+  for (int i = 0; i < 4; ++i) {
+    y.p[i] = __fmul2_rn(v.p[i], both(inv));
+    z.p[i] = __fadd2_rn(y.p[i], both(kMagic));
+    const float2 d = __ffma2_rn(__fadd2_rn(z.p[i], both(-kMagic)), both(-1.f), y.p[i]);
+    border = fmaxf(border, fmaxf(fabsf(d.x), fabsf(d.y)));
   }
-  if (border > 0.49998f) {
+  if (border > 0.5f - 0x1p-14f) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      w[i] = (uint32_t)(int)rint((double)v.at(i) * 127.0 / (double)a);
+    for (int i = 0; i < 8; ++i) {
+      const float c = z.at(i) - kMagic;
+      z.at(i) = settle(v.at(i) * down, a * down, c, y.at(i) - c) + kMagic;
+    }
   }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(z.at(i));
   const uint32_t lo = __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040),
                                   0x5410);
   const uint32_t hi = __byte_perm(__byte_perm(w[4], w[5], 0x0040), __byte_perm(w[6], w[7], 0x0040),
@@ -344,6 +456,22 @@ __device__ __forceinline__ Vals load_weights(const float* g, int l) {
 }
 
 }  // namespace rows
+
+// A kernel's opt-in to more than 48 KB of shared memory, once per device.
+class SmemOptIn {
+ public:
+  template <typename K>
+  cudaError_t set(K kernel, int bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && (done_.load() >> dev & 1))) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64) done_.fetch_or(1ull << dev);
+    return e;
+  }
+ private:
+  std::atomic<unsigned long long> done_{0};
+};
 
 // What the norm + rotation kernels are given, besides the layer's geometry.
 struct NormRopeArgs {

@@ -152,6 +152,7 @@ class _Fake:
     def __init__(self, t, device="cuda:0"):
         self.t, self.device = t, torch.device(device)
         self.shape, self.dtype, self.is_cuda = t.shape, t.dtype, True
+        self.get_device = lambda: self.device.index
 
     def __getattr__(self, name):
         return getattr(self.t, name)
