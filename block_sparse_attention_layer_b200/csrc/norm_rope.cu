@@ -40,6 +40,7 @@ struct Walk {
   FastDiv hw, w;                   // bh * bw, bw
   int chunk, chunks;               // rows of a chunk, chunks of a block
   int up;                          // units of heads of a CTA
+  int still;                       // whether some pairs do not turn
   uint32_t ld, kv_tok;             // bytes between tokens of the raw rows; positions of k and v
   long long kv_head;               // elements between heads of k and v
 };
@@ -91,11 +92,17 @@ struct Feed<E, D, true> {
 template <typename E, bool From8>
 constexpr int stages() { return From8 || sizeof(E) == 2 ? 3 : 2; }
 
+// Shared memory: the loads under way and their tokens, the column sums of the
+// CTA and those of its warps' lanes (one for each part of a row).
 template <typename E, int D, bool From8, bool TwoHeads>
-constexpr int smem_bytes() {
-  return stages<E, From8>() * kWarps * 2 * Feed<E, D, From8>::kBytes +
-         (TwoHeads ? 2 : 1) * (8 * kThreads + kMaxUp * D) * (int)sizeof(double);
-}
+struct Smem {
+  static constexpr int kNA = TwoHeads ? 2 : 1;
+  static constexpr int kLanes = kWarps * (D / 8);
+  static constexpr int kRing = stages<E, From8>() * kWarps * 2 * Feed<E, D, From8>::kBytes;
+  static constexpr int kSpots = stages<E, From8>() * kWarps * 8 * (int)sizeof(Spot);
+  static constexpr int kTotal = kMaxUp * kNA * D * (int)sizeof(double);
+  static constexpr int kBytes = kRing + kSpots + kTotal + kNA * 8 * kLanes * (int)sizeof(double);
+};
 
 template <typename E, int D, bool From8, bool To8, bool TwoHeads>
 __global__ void __launch_bounds__(kThreads, 2)
@@ -103,13 +110,14 @@ k_norm_rope(const __grid_constant__ Walk w, const __grid_constant__ NormRopeArgs
             const __grid_constant__ NormRopeOut o) {
   constexpr int G = D / 8, R = 32 / G, NA = TwoHeads ? 2 : 1;
   using F = Feed<E, D, From8>;
+  using M = Smem<E, D, From8, TwoHeads>;
   constexpr int S = stages<E, From8>();
   extern __shared__ __align__(16) char smem[];
-  double(&sums)[NA][8][kThreads] =               // a thread's fp64 column sums
-      *reinterpret_cast<double(*)[NA][8][kThreads]>(smem);
-  double* total = &sums[0][0][0] + NA * 8 * kThreads;    // the CTA's, read by its cluster
-  char* ring = reinterpret_cast<char*>(total + kMaxUp * NA * D) +
-               (threadIdx.x >> 5) * (S * 2 * F::kBytes);
+  char* ring = smem + (threadIdx.x >> 5) * (S * 2 * F::kBytes);
+  Spot* spots = reinterpret_cast<Spot*>(smem + M::kRing) + (threadIdx.x >> 5) * (S * 8);
+  double* total = reinterpret_cast<double*>(smem + M::kRing + M::kSpots);
+  double(&sums)[NA][8][M::kLanes] =
+      *reinterpret_cast<double(*)[NA][8][M::kLanes]>(total + kMaxUp * NA * D);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane / G, l = lane % G;
   const int h0 = (blockIdx.y * w.up + warp % w.up) * NA;
@@ -128,25 +136,40 @@ k_norm_rope(const __grid_constant__ Walk w, const __grid_constant__ NormRopeArgs
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       acc[u].at(i) = 0.f;
-      sums[u][i][threadIdx.x] = 0.0;
+      if (sub == 0) sums[u][i][warp * G + l] = 0.0;
     }
+  // adds the lanes' fp32 sums of a row part to its fp64 sums
+  auto flush = [&] {
+#pragma unroll
+    for (int u = 0; u < NA; ++u)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float v = acc[u].at(i);
+#pragma unroll
+        for (int m = G; m < 32; m <<= 1) v += __shfl_xor_sync(kAll, v, m);
+        if (sub == 0) sums[u][i][warp * G + l] += (double)v;
+        acc[u].at(i) = 0.f;
+      }
+  };
 
   const int stride = step * (TwoHeads ? 1 : 2);
   const int r_begin = first + warp / w.up * R;
   // row r of the block is token n = (t, y, x)
-  auto locate = [&](int r, int& t, int& y, int& x) {
+  auto locate = [&](int r) {
     const int bt = w.hw.div(r), rest = r - bt * (w.bh * w.bw), by = w.w.div(rest);
-    t = t0 + bt;
-    y = y0 + by;
-    x = x0 + rest - by * w.bw;
-    return (t * w.H + y) * w.W + x;
+    const int t = t0 + bt, y = y0 + by, x = x0 + rest - by * w.bw;
+    return Spot{{t * a.ht, y_rows + y * a.hh, x_rows + x * a.hw}, (t * w.H + y) * w.W + x};
   };
   auto ask = [&](int r0, int stage) {
     if (r0 < last) {
-      int n = 0, t, y, x;
+      int n = 0;
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        if (!TwoHeads || u == 0) n = locate(min(r0 + u * step + sub, last - 1), t, y, x);
+        if (!TwoHeads || u == 0) {
+          const Spot spot = locate(min(r0 + u * step + sub, last - 1));
+          n = spot.n;
+          if (l == 0) spots[stage * 8 + u * 4 + sub] = spot;
+        }
         F::ask(ring + (stage * 2 + u) * F::kBytes, w, a, n, h0 + (TwoHeads ? u : 0), lane, l);
       }
     }
@@ -156,7 +179,9 @@ k_norm_rope(const __grid_constant__ Walk w, const __grid_constant__ NormRopeArgs
   for (int i = 0; i < S - 1; ++i) ask(r_begin + i * stride, i);
   int rows = 0, stage = 0;
   for (int r0 = r_begin; r0 < last; r0 += stride) {
+    __syncwarp();                    // the spots of the stage that is refilled have been read
     ask(r0 + (S - 1) * stride, stage == 0 ? S - 1 : stage - 1);
+    __syncwarp();                    // and this stage's, written S - 1 steps ago, are visible
     int r[2], n[2];
     bool mine[2];
     float2 cs[TwoHeads ? 1 : 2][4];
@@ -167,9 +192,9 @@ k_norm_rope(const __grid_constant__ Walk w, const __grid_constant__ NormRopeArgs
       } else {
         r[u] = r0 + u * step + sub;
         mine[u] = r[u] < last;
-        int t, y, x;
-        n[u] = locate(min(r[u], last - 1), t, y, x);
-        load_turns(refs, a.table, t * a.ht, y_rows + y * a.hh, x_rows + x * a.hw, cs[u]);
+        const Spot* spot = spots + stage * 8 + u * 4 + sub;
+        n[u] = spot->n;
+        load_turns(refs, a.table, w.still, spot, cs[u]);
       }
     }
     fetch_wait<S - 1>();
@@ -237,68 +262,110 @@ k_norm_rope(const __grid_constant__ Walk w, const __grid_constant__ NormRopeArgs
     rows += TwoHeads ? 1 : 2;
     if (rows >= kFlush) {
       rows = 0;
-#pragma unroll
-      for (int u = 0; u < NA; ++u)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          sums[u][i][threadIdx.x] += (double)acc[u].at(i);
-          acc[u].at(i) = 0.f;
-        }
+      flush();
     }
   }
   if (o.blocks == nullptr) return;
-#pragma unroll
-  for (int u = 0; u < NA; ++u)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sums[u][i][threadIdx.x] += (double)acc[u].at(i);
+  flush();
   __syncthreads();
   const int cols = w.up * NA * D;
+  auto write = [&](int c, double sum) {
+    o.blocks[((size_t)(blockIdx.y * w.up * NA + c / D) * w.Nb + j) * D + c % D] =
+        (float)(sum / (double)w.L);
+  };
   for (int c = threadIdx.x; c < cols; c += kThreads) {
     const int hh = c / D, i = c % D / G, ll = c % G;      // lanes apart: no bank conflicts
     double sum = 0.0;
     for (int v = hh / NA; v < kWarps; v += w.up)
-#pragma unroll
-      for (int b = 0; b < R; ++b) sum += sums[hh % NA][i][v * 32 + b * G + ll];
-    total[hh * D + elem_at<E, D>(ll, i)] = sum;
+      sum += sums[hh % NA][i][v * G + ll];
+    const int col = hh * D + elem_at<E, D>(ll, i);
+    if (w.chunks == 1)
+      write(col, sum);
+    else
+      total[col] = sum;
   }
+  if (w.chunks == 1) return;
   cg::cluster_group cluster = cg::this_cluster();
   cluster.sync();
-  const int rank = cluster.block_rank(), size = cluster.num_blocks();
-  for (int c = rank * kThreads + threadIdx.x; c < cols; c += size * kThreads) {
+  const int rank = cluster.block_rank();
+  for (int c = rank * kThreads + threadIdx.x; c < cols; c += w.chunks * kThreads) {
     double sum = 0.0;
-    for (int m = 0; m < size; ++m) sum += cluster.map_shared_rank(total, m)[c];
-    o.blocks[((size_t)(blockIdx.y * w.up * NA + c / D) * w.Nb + j) * D + c % D] =
-        (float)(sum / (double)w.L);
+    for (int m = 0; m < w.chunks; ++m) sum += cluster.map_shared_rank(total, m)[c];
+    write(c, sum);
   }
   cluster.sync();                    // a member's sums are read until here
 }
+
+// CTAs of a kernel that the device runs at once in clusters of each size
+// (clusters do not cross GPCs, whose sizes differ), asked once per device.
+class Capacity {
+ public:
+  template <typename K>
+  int ctas(K kernel, int cluster, int smem, int num_sms) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return num_sms;
+    std::atomic<int>& known = known_[dev][cluster];
+    int n = known.load(std::memory_order_relaxed);
+    if (n) return n;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(cluster);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = cluster;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+      (void)cudaGetLastError();
+      return num_sms;
+    }
+    known.store(n * cluster, std::memory_order_relaxed);
+    return n * cluster;
+  }
+
+ private:
+  static constexpr int kDevices = 16;
+  std::atomic<int> known_[kDevices][9] = {};
+};
 
 template <typename E, int D, bool From8, bool To8, bool TwoHeads>
 cudaError_t launch_t(const Prob& P, const NormRopeArgs& a, const NormRopeOut& o, int num_sms,
                      cudaStream_t st) {
   constexpr int R = 256 / D;
+  using M = Smem<E, D, From8, TwoHeads>;
+  const auto kernel = k_norm_rope<E, D, From8, To8, TwoHeads>;
+  static SmemOptIn opt_in;
+  static Capacity capacity;
+  cudaError_t e = opt_in.set(kernel, M::kBytes);
+  if (e != cudaSuccess) return e;
   const int units = TwoHeads ? P.n_h / 2 : P.n_h;
   Walk w{};
   w.T = P.T; w.H = P.H; w.W = P.W; w.n_h = P.n_h;
   w.bt = P.bt; w.bh = P.bh; w.bw = P.bw;
   w.nbh = P.nbh; w.nbw = P.nbw; w.Nb = P.Nb; w.L = P.L;
   w.ld = (uint32_t)(a.ld * sizeof(E));
-  w.up = units % 2 == 0 ? 2 : 1;
-  const int step = kWarps / w.up * R, groups = units / w.up;
+  w.still = 2 * (a.ht + a.hh + a.hw) < D;
   if (o.blocks) {
     w.kv_tok = D * sizeof(E);
     w.kv_head = (long long)P.s * D;
-    // the chunk count whose CTAs, two on an SM at a time, get through the
-    // steps of the slowest slot first; each further CTA of a slot costs about
-    // two steps of filling and reducing
-    const int slots = 2 * num_sms;
+    // the units and chunks of a CTA for which the slowest of the places that
+    // CTAs run in has the fewest steps; a CTA's filling and reducing costs
+    // about two
     long long best = -1;
-    for (int c = 1; c <= 8; ++c) {
-      const long long waves = ((long long)P.Nb * c * groups + slots - 1) / slots;
-      const long long cost = waves * (((P.L + c - 1) / c + step - 1) / step + 2);
-      if (best < 0 || cost < best) {
-        best = cost;
-        w.chunks = c;
+    for (int up = units % 2 == 0 ? 2 : 1; up >= 1; --up) {
+      const int step = kWarps / up * R;
+      for (int c = 1; c <= 8 && c <= P.L; ++c) {
+        const long long ctas = (long long)P.Nb * c * (units / up);
+        const int slots = capacity.ctas(kernel, c, M::kBytes, num_sms);
+        const long long cost =
+            ((ctas + slots - 1) / slots) * (((P.L + c - 1) / c + step - 1) / step + 2);
+        if (best < 0 || cost < best) {
+          best = cost;
+          w.up = up;
+          w.chunks = c;
+        }
       }
     }
     w.chunk = (P.L + w.chunks - 1) / w.chunks;
@@ -308,7 +375,9 @@ cudaError_t launch_t(const Prob& P, const NormRopeArgs& a, const NormRopeOut& o,
     w.L = P.s;
     w.kv_tok = P.n_h * D * sizeof(E);
     w.kv_head = D;
-    const long long want = 8LL * num_sms / groups + 1;
+    w.up = units % 2 == 0 ? 2 : 1;
+    const int step = kWarps / w.up * R;
+    const long long want = 8LL * num_sms * w.up / units + 1;
     w.chunk = (int)((P.s + want - 1) / want);
     w.chunk = (w.chunk + step - 1) / step * step;
     w.chunks = (P.s + w.chunk - 1) / w.chunk;
@@ -316,9 +385,9 @@ cudaError_t launch_t(const Prob& P, const NormRopeArgs& a, const NormRopeOut& o,
   w.hw = FastDiv(w.bh * w.bw);
   w.w = FastDiv(w.bw);
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(w.Nb * w.chunks, groups);
+  cfg.gridDim = dim3(w.Nb * w.chunks, units / w.up);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem_bytes<E, D, From8, TwoHeads>();
+  cfg.dynamicSmemBytes = M::kBytes;
   cfg.stream = st;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -326,10 +395,6 @@ cudaError_t launch_t(const Prob& P, const NormRopeArgs& a, const NormRopeOut& o,
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  const auto kernel = k_norm_rope<E, D, From8, To8, TwoHeads>;
-  static SmemOptIn opt_in;
-  cudaError_t e = opt_in.set(kernel, (int)cfg.dynamicSmemBytes);
-  if (e != cudaSuccess) return e;
   {
     VMOBA_TRACE("k_norm_rope", st);
     e = cudaLaunchKernelEx(&cfg, kernel, w, a, o);

@@ -6,8 +6,11 @@
 // projection's output or from its 8-bit checkpoint.  HBM bound: 8 s n_h d
 // elements (two of them bytes when x is a checkpoint).
 //
-// A CTA walks chunks of tokens of one head; each lane keeps fp32 sums of its
-// weight gradients over a chunk (at most kChunk / 16 rows) and adds them to
+// As in the forward, a lane works on two rows of q, k (and v) at a time, two
+// neighbouring heads of a token where the head count is even, fed through
+// shared memory by asynchronous copies one step ahead.  CTAs stay resident
+// and walk items of neighbouring tokens of one unit of heads.  Each lane keeps
+// fp32 sums of its weight gradients over at most kFlush rows and adds them to
 // fp64 sums in shared memory, the CTA's total goes to the workspace, and a
 // second kernel adds the totals in a fixed order, so results do not depend on
 // scheduling.
@@ -20,14 +23,42 @@ using namespace rows;
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kChunk = 256;         // tokens of one work item
+constexpr int kFlush = 64;          // rows a lane adds in fp32 before they go to its fp64 sums
 constexpr int kMaxCtas = 1024;      // partial weight gradients in the workspace
 
 struct Walk {
   int T, H, W, s, n_h;
+  int chunk, still;                // tokens of a work item; whether some pairs do not turn
   FastDiv hw, w;                   // H * W, W
   uint32_t ld, ld_out;             // bytes between tokens
   int n_items, n_chunks;
+};
+
+// The gradients and the raw q and k of one row on their way through shared
+// memory.
+template <typename E, int D, bool From8>
+struct Feed {
+  static constexpr int kSlot = Slot<E, D>::kBytes;
+  static constexpr int kRaw = From8 ? Slot8<E, D>::kBytes : kSlot;
+  static constexpr int kBytes = 3 * kSlot + 2 * kRaw;
+  __device__ __forceinline__ static Vals raw(const char* s, int i, int lane) {
+    s += 3 * kSlot + i * kRaw;
+    if constexpr (From8)
+      return decode8(Slot8<E, D>::codes(s, lane), Slot8<E, D>::scale(s, lane));
+    else
+      return unpack(Slot<E, D>::get(s, lane));
+  }
+};
+
+// Iterations a warp's loads run ahead.
+constexpr int kStages = 2;
+
+template <typename E, int D, bool From8>
+struct Smem {
+  static constexpr int kRing = kStages * kWarps * 2 * Feed<E, D, From8>::kBytes;
+  static constexpr int kSpots = kStages * kWarps * 8 * (int)sizeof(Spot);
+  static constexpr int kLanes = kWarps * (D / 8);      // lanes of one row in every warp
+  static constexpr int kBytes = kRing + kSpots + 16 * kLanes * (int)sizeof(double);
 };
 
 template <typename E, int D, bool From8, bool TwoHeads>
@@ -35,78 +66,128 @@ __global__ void __launch_bounds__(kThreads, 2)
 k_norm_rope_bwd(const __grid_constant__ Walk w, const __grid_constant__ NormRopeArgs a,
                 const E* __restrict__ dq, const E* __restrict__ dk, const E* __restrict__ dv,
                 E* __restrict__ oq, E* __restrict__ ok, E* __restrict__ ov, float* part) {
-  constexpr int G = D / 8, R = 32 / G;
-  __shared__ double sums[16][kThreads];
+  constexpr int G = D / 8, R = 32 / G, S = kStages;
+  constexpr int kStep = kWarps * R, kStride = kStep * (TwoHeads ? 1 : 2);
+  using F = Feed<E, D, From8>;
+  using M = Smem<E, D, From8>;
+  extern __shared__ __align__(16) char smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane / G, l = lane % G;
+  char* ring = smem + warp * (S * 2 * F::kBytes);
+  Spot* spots = reinterpret_cast<Spot*>(smem + M::kRing) + warp * (S * 8);
+  double(&sums)[16][M::kLanes] =
+      *reinterpret_cast<double(*)[16][M::kLanes]>(smem + M::kRing + M::kSpots);
   const Vals gq = load_weights<E, D>(a.gq, l), gk = load_weights<E, D>(a.gk, l);
   const PairRefs refs = pair_refs<E, D>(l, a.ht, a.hh, a.hw);
   const int y_rows = w.T * a.ht, x_rows = y_rows + w.H * a.hh;
   const uint32_t row3 = w.n_h * D * sizeof(E);
+  if (sub == 0) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) sums[i][threadIdx.x] = 0.0;
+    for (int i = 0; i < 16; ++i) sums[i][warp * G + l] = 0.0;
+  }
 
-  for (int item = blockIdx.x; item < w.n_items; item += gridDim.x) {
-    const int unit = item / w.n_chunks, c0 = (item - unit * w.n_chunks) * kChunk;
-    const int h0 = unit * (TwoHeads ? 2 : 1);
-    const int last = min(c0 + kChunk, w.s);
-    Vals wq, wk;
+  // A warp walks the tokens of its CTA's items as one sequence, so that its
+  // loads run ahead over the end of an item too.
+  struct At {
+    int item, n0, last, h0;
+  };
+  auto enter = [&](At& p) {          // the warp's first token of the item
+    if (p.item >= w.n_items) return;
+    const int unit = p.item / w.n_chunks, c0 = (p.item - unit * w.n_chunks) * w.chunk;
+    p.h0 = unit * (TwoHeads ? 2 : 1);
+    p.n0 = c0 + warp * R;
+    p.last = min(c0 + w.chunk, w.s);
+  };
+  auto skip_empty = [&](At& p) {     // an item may have no token for this warp
+    while (p.item < w.n_items && p.n0 >= p.last) {
+      p.item += gridDim.x;
+      enter(p);
+    }
+  };
+  At cur{(int)blockIdx.x, 0, 0, 0};
+  enter(cur);
+  skip_empty(cur);
+  At ahead = cur;
+  auto ask = [&](int stage) {
+    if (ahead.item < w.n_items) {
+      int n = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) wq.p[i] = wk.p[i] = both(0.f);
-    constexpr int kStep = kWarps * R;
-    for (int n0 = c0 + warp * R; n0 < last; n0 += kStep * (TwoHeads ? 1 : 2)) {
+      for (int u = 0; u < 2; ++u) {
+        if (!TwoHeads || u == 0) {
+          n = min(ahead.n0 + u * kStep + sub, ahead.last - 1);
+          if (l == 0) {
+            const int t = w.hw.div(n), yx = n - t * (w.H * w.W), y = w.w.div(yx);
+            spots[stage * 8 + u * 4 + sub] =
+                Spot{{t * a.ht, y_rows + y * a.hh, x_rows + (yx - y * w.W) * a.hw}, n};
+          }
+        }
+        const int h = ahead.h0 + (TwoHeads ? u : 0);
+        char* to = ring + (stage * 2 + u) * F::kBytes;
+        Slot<E, D>::ask(to, at_bytes(dq + h * D, n, row3), lane, l);
+        Slot<E, D>::ask(to + F::kSlot, at_bytes(dk + h * D, n, row3), lane, l);
+        Slot<E, D>::ask(to + 2 * F::kSlot, at_bytes(dv + h * D, n, row3), lane, l);
+        to += 3 * F::kSlot;
+        if constexpr (From8) {
+          const uint32_t row = (uint32_t)(n * 3 * w.n_h + h);
+          Slot8<E, D>::ask(to, at_bytes(a.codes, row, D), a.scales + row, lane, l);
+          Slot8<E, D>::ask(to + F::kRaw, at_bytes(a.codes, row + w.n_h, D),
+                           a.scales + row + w.n_h, lane, l);
+        } else {
+          Slot<E, D>::ask(to, at_bytes(static_cast<const E*>(a.in[0]) + h * D, n, w.ld), lane, l);
+          Slot<E, D>::ask(to + F::kRaw, at_bytes(static_cast<const E*>(a.in[1]) + h * D, n, w.ld),
+                          lane, l);
+        }
+      }
+      ahead.n0 += kStride;
+      skip_empty(ahead);
+    }
+    fetch_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < S - 1; ++i) ask(i);
+  int stage = 0;
+  Vals wq, wk;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) wq.p[i] = wk.p[i] = both(0.f);
+  int rows = 0;
+  while (cur.item < w.n_items) {
+    {
+      __syncwarp();                  // the spots of the stage that is refilled have been read
+      ask(stage == 0 ? S - 1 : stage - 1);
+      __syncwarp();                  // and this stage's are visible
       int n[2];
       bool mine[2];
       float2 cs[TwoHeads ? 1 : 2][4];
-      Raw<E> uq[2], uk[2], uv[2];
-      Vals x[4];
-      [[maybe_unused]] Raw<E> xq[2], xk[2];
-      [[maybe_unused]] uint2 cq[2], ck[2];
-      [[maybe_unused]] float sq[2], sk[2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         if (TwoHeads && u == 1) {
           n[1] = n[0]; mine[1] = mine[0];
         } else {
-          mine[u] = n0 + u * kStep + sub < last;
-          n[u] = min(n0 + u * kStep + sub, last - 1);
-          const int t = w.hw.div(n[u]), yx = n[u] - t * (w.H * w.W), y = w.w.div(yx);
-          load_turns(refs, a.table, t * a.ht, y_rows + y * a.hh, x_rows + (yx - y * w.W) * a.hw,
-                     cs[u]);
-        }
-        const int h = h0 + (TwoHeads ? u : 0);
-        uq[u] = load_row<D>(at_bytes(dq + h * D, n[u], row3), l);
-        uk[u] = load_row<D>(at_bytes(dk + h * D, n[u], row3), l);
-        uv[u] = load_row<D>(at_bytes(dv + h * D, n[u], row3), l);
-        if constexpr (From8) {
-          const uint32_t row = (uint32_t)(n[u] * 3 * w.n_h + h);
-          cq[u] = load_codes<E, D>(at_bytes(a.codes, row, D), l);
-          ck[u] = load_codes<E, D>(at_bytes(a.codes, row + w.n_h, D), l);
-          sq[u] = __ldg(a.scales + row);
-          sk[u] = __ldg(a.scales + row + w.n_h);
-        } else {
-          xq[u] = load_row<D>(at_bytes(static_cast<const E*>(a.in[0]) + h * D, n[u], w.ld), l);
-          xk[u] = load_row<D>(at_bytes(static_cast<const E*>(a.in[1]) + h * D, n[u], w.ld), l);
+          mine[u] = cur.n0 + u * kStep + sub < cur.last;
+          const Spot* spot = spots + stage * 8 + u * 4 + sub;
+          n[u] = spot->n;
+          load_turns(refs, a.table, w.still, spot, cs[u]);
         }
       }
+      const int h0 = cur.h0;
+      fetch_wait<S - 1>();
+      const char* in[2] = {ring + stage * 2 * F::kBytes, ring + (stage * 2 + 1) * F::kBytes};
+      stage = stage == S - 1 ? 0 : stage + 1;
+      Vals x[4];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        if constexpr (From8) {
-          x[2 * u] = decode8(cq[u], sq[u]);
-          x[2 * u + 1] = decode8(ck[u], sk[u]);
-        } else {
-          x[2 * u] = unpack(xq[u]);
-          x[2 * u + 1] = unpack(xk[u]);
-        }
+        x[2 * u] = F::raw(in[u], 0, lane);
+        x[2 * u + 1] = F::raw(in[u], 1, lane);
         if (mine[u])
-          store_raw<D>(at_bytes(ov + (h0 + (TwoHeads ? u : 0)) * D, n[u], w.ld_out), l, uv[u]);
+          store_raw<D>(at_bytes(ov + (h0 + (TwoHeads ? u : 0)) * D, n[u], w.ld_out), l,
+                       Slot<E, D>::get(in[u] + 2 * F::kSlot, lane));
       }
       float r[4], pre[4], dot[4];
       inv_rms<D>(x, a.eps, l, r, pre);
       Vals g[4];                                // the gradients, then w = u g
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        g[k] = unpack(k & 1 ? uk[k / 2] : uq[k / 2]);
+        g[k] = unpack(Slot<E, D>::get(in[k / 2] + (k & 1) * F::kSlot, lane));
         turn_back(g[k], cs[TwoHeads ? 0 : k / 2]);
         Vals& sum = k & 1 ? wk : wq;
 #pragma unroll
@@ -132,21 +213,28 @@ k_norm_rope_bwd(const __grid_constant__ Walk w, const __grid_constant__ NormRope
         }
       }
     }
+    cur.n0 += kStride;
+    skip_empty(cur);
+    if ((rows += 2) < kFlush && cur.item < w.n_items) continue;
+    rows = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      sums[i][threadIdx.x] += (double)wq.at(i);
-      sums[8 + i][threadIdx.x] += (double)wk.at(i);
+    for (int i = 0; i < 16; ++i) {
+      float v = i < 8 ? wq.at(i) : wk.at(i - 8);
+#pragma unroll
+      for (int o = G; o < 32; o <<= 1) v += __shfl_xor_sync(kAll, v, o);
+      if (sub == 0) sums[i][warp * G + l] += (double)v;
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) wq.p[i] = wk.p[i] = both(0.f);
   }
   if (part == nullptr) return;
   __syncthreads();
-  // column e of the q and k gradients: element i of lane ll, over warps and rows
+  // column e of the q and k gradients: element i of lane ll, over the warps
   for (int c = threadIdx.x; c < 2 * D; c += kThreads) {
     const int which = c / D, i = c % D / G, ll = c % G;
     double sum = 0.0;
-    for (int v = 0; v < kWarps; ++v)
 #pragma unroll
-      for (int b = 0; b < R; ++b) sum += sums[8 * which + i][v * 32 + b * G + ll];
+    for (int v = 0; v < kWarps; ++v) sum += sums[8 * which + i][v * G + ll];
     part[(size_t)blockIdx.x * 2 * D + which * D + elem_at<E, D>(ll, i)] = (float)sum;
   }
 }
@@ -179,13 +267,24 @@ cudaError_t launch_t(const Prob& P, const NormRopeArgs& a, const void* dq, const
   w.w = FastDiv(P.W);
   w.ld = (uint32_t)(a.ld * sizeof(E));
   w.ld_out = (uint32_t)(ld_out * sizeof(E));
-  w.n_chunks = (P.s + kChunk - 1) / kChunk;
-  w.n_items = w.n_chunks * (TwoHeads ? P.n_h / 2 : P.n_h);
-  const int ctas = min(min(w.n_items, num_sms * 2), kMaxCtas);
+  // items of one stride of the CTA's warps up to sixteen, so that two CTAs on
+  // every SM have one where the tokens suffice
+  constexpr int stride = kWarps * (256 / D) * (TwoHeads ? 1 : 2);
+  const int units = TwoHeads ? P.n_h / 2 : P.n_h, slots = min(2 * num_sms, kMaxCtas);
+  const long long share = (long long)P.s * units / slots / stride;
+  w.chunk = stride * (int)max(1LL, min(16LL, share));
+  w.n_chunks = (P.s + w.chunk - 1) / w.chunk;
+  w.n_items = w.n_chunks * units;
+  w.still = 2 * (a.ht + a.hh + a.hw) < D;
+  const int ctas = min(w.n_items, slots);
   float* part = dweight ? static_cast<float*>(ws) : nullptr;
+  const auto kernel = k_norm_rope_bwd<E, D, From8, TwoHeads>;
+  constexpr int smem = Smem<E, D, From8>::kBytes;
+  static SmemOptIn opt_in;
+  if (const cudaError_t e = opt_in.set(kernel, smem); e != cudaSuccess) return e;
   {
     VMOBA_TRACE("k_norm_rope_bwd", st);
-    k_norm_rope_bwd<E, D, From8, TwoHeads><<<ctas, kThreads, 0, st>>>(
+    kernel<<<ctas, kThreads, smem, st>>>(
         w, a, static_cast<const E*>(dq), static_cast<const E*>(dk), static_cast<const E*>(dv),
         static_cast<E*>(out[0]), static_cast<E*>(out[1]), static_cast<E*>(out[2]), part);
   }

@@ -213,6 +213,21 @@ __device__ __forceinline__ void spread(float s, float (&v)[4]) {
   for (int k = 0; k < 4; ++k) v[k] = __shfl_sync(kAll, s, k * (G / 4), G);
 }
 
+// The same for two rows; sum k is with lane k * G / 2 of the group.
+template <int G>
+__device__ __forceinline__ float half_sums(const float (&v)[2], int l) {
+  const bool hi = l & (G / 2);
+  float s = (hi ? v[1] : v[0]) + __shfl_xor_sync(kAll, hi ? v[0] : v[1], G / 2);
+#pragma unroll
+  for (int o = G / 4; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
+  return s;
+}
+template <int G>
+__device__ __forceinline__ void spread(float s, float (&v)[2]) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) v[k] = __shfl_sync(kAll, s, k * (G / 2), G);
+}
+
 // Sum over the G lanes of a row.
 template <int G>
 __device__ __forceinline__ float row_sum(float v) {
@@ -292,7 +307,11 @@ __device__ __forceinline__ uint2 encode8(const Vals& v, uint32_t m, float& scale
     scale = m >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : 0.f;
     return make_uint2(0u, 0u);
   }
-  scale = a / 127.0f;
+  // a / 127 correctly rounded: a first quotient and one step with its exact
+  // remainder (Markstein's division; checked against a / 127 for every mantissa)
+  constexpr float kInv = 1.0f / 127.0f;
+  const float q = a * kInv;
+  scale = fmaf(fmaf(-127.0f, q, a), kInv, q);
   // 127 a stays finite, and its reciprocal normal, with a large a scaled down
   const float down = a > 0x1p100f ? 0x1p-8f : 1.0f;
   float inv;
@@ -359,26 +378,35 @@ __device__ __forceinline__ void store_codes(int8_t* row, int l, uint2 c) {
 
 // ---- norm ----
 
-// r[k] = 1 / sqrt(mean x^2 + eps) of four rows.  Where a row's squares leave
-// fp32's range it is first scaled by pre[k] = 2^-80 (x changes; eps then is
-// far below the mean's last bit); else pre[k] = 1.
-template <int D>
-__device__ __forceinline__ void inv_rms(Vals (&x)[4], float eps, int l, float (&r)[4],
-                                        float (&pre)[4]) {
+// 1 / sqrt(v) within 2 ulp; v is never subnormal here (eps >= 1e-30).
+__device__ __forceinline__ float rsqrt_normal(float v) {
+  float r;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// r[k] = 1 / sqrt(mean x^2 + eps) of two or four rows.  Where a row's squares
+// leave fp32's range it is first scaled by pre[k] = 2^-80 (x changes; eps then
+// is far below the mean's last bit); else pre[k] = 1.
+template <int D, int N>
+__device__ __forceinline__ void inv_rms(Vals (&x)[N], float eps, int l, float (&r)[N],
+                                        float (&pre)[N]) {
   constexpr int G = D / 8;
-  float ss[4];
+  float ss[N];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
+  for (int k = 0; k < N; ++k) {
     ss[k] = lane_dot(x[k], x[k]);
     pre[k] = 1.f;
   }
-  const float s = quarter_sums<G>(ss, l);
-  spread<G>(rsqrtf(fmaf(s, 1.0f / D, eps)), r);
+  float s;
+  if constexpr (N == 4) s = quarter_sums<G>(ss, l);
+  else s = half_sums<G>(ss, l);
+  spread<G>(rsqrt_normal(fmaf(s, 1.0f / D, eps)), r);
   if (__any_sync(kAll, !(s < 0x1p100f))) {
-    float sum[4];
+    float sum[N];
     spread<G>(s, sum);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < N; ++k) {
       const bool big = !(sum[k] < 0x1p100f);
       if (big) {
         pre[k] = 0x1p-80f;
@@ -386,46 +414,57 @@ __device__ __forceinline__ void inv_rms(Vals (&x)[4], float eps, int l, float (&
         for (int i = 0; i < 8; ++i) x[k].at(i) *= 0x1p-80f;
       }
       const float again = row_sum<G>(lane_dot(x[k], x[k]));
-      if (big) r[k] = rsqrtf(again * (1.0f / D));
+      if (big) r[k] = rsqrt_normal(again * (1.0f / D));
     }
   }
 }
 
 // ---- rotation ----
 
-// Where a lane's four pairs find their table entry: the pair's place in its
-// axis part and the axis (0, 1, 2 = t, y, x; 3 = the pair stays), two bits each.
+// A token's place as the lanes of its row share it, in shared memory: the
+// table rows of its t, y and x and its index.
+struct __align__(16) Spot {
+  int row[3];
+  int n;
+};
+
+// Where a lane's four pairs find their table entry: the axis whose table row
+// counts (0, 1, 2 = t, y, x) and the pair's place in that row; `still` has a
+// bit for each pair that does not turn.
 struct PairRefs {
-  int place[4];
-  uint32_t axes;
+  int place[4], axis[4];
+  uint32_t still;
 };
 
 template <typename E, int D>
 __device__ __forceinline__ PairRefs pair_refs(int l, int ht, int hh, int hw) {
   PairRefs r;
-  r.axes = 0u;
+  r.still = 0u;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     int p = elem_at<E, D>(l, 2 * i) / 2;
-    uint32_t axis = 0u;
-    if (p >= ht) { p -= ht; axis = 1u; }
-    if (axis == 1u && p >= hh) { p -= hh; axis = 2u; }
-    if (axis == 2u && p >= hw) axis = 3u;
+    int axis = 0;
+    if (p >= ht) { p -= ht; axis = 1; }
+    if (axis == 1 && p >= hh) { p -= hh; axis = 2; }
+    if (axis == 2 && p >= hw) { p = 0; r.still |= 1u << i; }
     r.place[i] = p;
-    r.axes |= axis << (2 * i);
+    r.axis[i] = axis;
   }
   return r;
 }
 
-// rt, ry, rx: the table rows of the token's t, y and x.
-__device__ __forceinline__ void load_turns(const PairRefs& r, const float2* table, int rt, int ry,
-                                           int rx, float2 (&cs)[4]) {
+// some_still: whether any pair of a head stays (then the entry read for it,
+// if the table has one at all, is replaced by no turn).
+__device__ __forceinline__ void load_turns(const PairRefs& r, const float2* table, bool some_still,
+                                           const Spot* spot, float2 (&cs)[4]) {
+  if (some_still) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t axis = (r.axes >> (2 * i)) & 3u;
-    const int row = axis == 0u ? rt : (axis == 1u ? ry : rx);
-    cs[i] = make_float2(1.f, 0.f);
-    if (axis < 3u) cs[i] = __ldg(table + row + r.place[i]);
+    for (int i = 0; i < 4; ++i)
+      cs[i] = r.still >> i & 1u ? make_float2(1.f, 0.f)
+                                : __ldg(table + spot->row[r.axis[i]] + r.place[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) cs[i] = __ldg(table + spot->row[r.axis[i]] + r.place[i]);
   }
 }
 
