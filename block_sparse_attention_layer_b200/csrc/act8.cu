@@ -100,7 +100,7 @@ k_act8_pack(const E* __restrict__ x, const __grid_constant__ Shape s, int8_t* __
       const int k = (u + b) * kPer + threadIdx.x / G;
       if (k >= most) continue;
       float scale;
-      const uint2 w = encode8(unpack(r[u + b]), m[b], scale);
+      const uint2 w = encode8<E>(unpack(r[u + b]), m[b], scale);
       if (l == 0) scales[base + k] = scale;
       int8_t* dst = codes + at[u + b].row * s.cols;
       if constexpr (Vec) {

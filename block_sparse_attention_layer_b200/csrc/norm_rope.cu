@@ -215,7 +215,7 @@ k_norm_rope(const __grid_constant__ Walk w, const __grid_constant__ NormRopeArgs
         uint2 c[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u)
-          c[u] = encode8(i < 2 ? x[2 * u + i] : unpack(raw[2 + 3 * u]), m[i + 3 * u], sc[u]);
+          c[u] = encode8<E>(i < 2 ? x[2 * u + i] : unpack(raw[2 + 3 * u]), m[i + 3 * u], sc[u]);
         const uint32_t row[2] = {(uint32_t)((n[0] * 3 + i) * w.n_h + h0),
                                  (uint32_t)((n[1] * 3 + i) * w.n_h + h0 + (TwoHeads ? 1 : 0))};
 #pragma unroll

@@ -254,18 +254,23 @@ __device__ __forceinline__ float lane_dot(const Vals& a, const Vals& b) {
 // Group maxima of |x| as bits: an infinity or NaN sorts above every finite
 // value.  bf16 works on the stored 16 bits, two values an instruction, and
 // two groups share the words of one shuffle tree.
+__device__ __forceinline__ uint32_t max16x2(uint32_t a, uint32_t b) {
+  uint32_t m;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(b));
+  return m;
+}
 __device__ __forceinline__ uint32_t lane_max(const Raw<__nv_bfloat16>& r) {
   constexpr uint32_t kAbs = 0x7FFF7FFFu;
-  return __vmaxu2(__vmaxu2(r.u.x & kAbs, r.u.y & kAbs), __vmaxu2(r.u.z & kAbs, r.u.w & kAbs));
+  return max16x2(max16x2(r.u.x & kAbs, r.u.y & kAbs), max16x2(r.u.z & kAbs, r.u.w & kAbs));
 }
 template <int G>
 __device__ __forceinline__ void group_max(const Raw<__nv_bfloat16>& a,
                                           const Raw<__nv_bfloat16>& b, uint32_t& ma,
                                           uint32_t& mb) {
   const uint32_t wa = lane_max(a), wb = lane_max(b);
-  uint32_t m = __vmaxu2(__byte_perm(wa, wb, 0x5410), __byte_perm(wa, wb, 0x7632));
+  uint32_t m = max16x2(__byte_perm(wa, wb, 0x5410), __byte_perm(wa, wb, 0x7632));
 #pragma unroll
-  for (int o = G / 2; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(kAll, m, o));
+  for (int o = G / 2; o > 0; o >>= 1) m = max16x2(m, __shfl_xor_sync(kAll, m, o));
   ma = m << 16;
   mb = m & 0xFFFF0000u;
 }
@@ -295,53 +300,73 @@ __device__ __forceinline__ float settle(float x, float a, float c, float d) {
   return s > 0.f ? T + 0.5f : (s < 0.f ? T - 0.5f : 2.0f * rintf(0.5f * T));
 }
 
+__device__ __forceinline__ float max_abs3(float a, float b, float c) {
+  float m;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(fabsf(b)), "f"(fabsf(c)));
+  return m;
+}
+
 // Codes of a lane's eight values, byte i = element i, for a group whose
-// max |x| has the bits `m`; scale gets the group's.  The quotient is taken
-// as x * (127 / a) in fp32, off by less than 2^-14 (reciprocal, two products:
-// 4 * 2^-24 relative of at most 127), and rounded by adding 1.5 * 2^23; where
-// one lands that close to a rounding border the lane settles its eight
-// exactly.
+// max |x| has the bits `m`; scale gets the group's.  The quotient is x *
+// (127 / a) with the factor in fp32 (reciprocal, product: off by less than
+// 2^-22 of it), rounded to an integer by the fma that adds 1.5 * 2^23.
+//
+// bf16: x and a have eight bits each, so a quotient that is no tie is at least
+// 2^-16 of itself away from one, and unless a's significand is 254 / 128 the
+// only tie is 63.5 (x = a / 2), which goes up to 64.  A factor 2^-19 larger
+// than 127 / a therefore rounds every quotient as asked (checked for every
+// pair of significands); with 254 / 128 each value is settled exactly.
+// fp32: where a quotient's distance from its integer is so close to a half
+// that the factor's error could decide, the lane settles its eight.
+template <typename E>
 __device__ __forceinline__ uint2 encode8(const Vals& v, uint32_t m, float& scale) {
   const float a = __uint_as_float(m);
-  if (m >= 0x7F800000u || a < 0x1p-119f) {
-    scale = m >= 0x7F800000u ? __uint_as_float(0x7FC00000u) : 0.f;
-    return make_uint2(0u, 0u);
-  }
+  const bool bad = m >= 0x7F800000u, none = a < 0x1p-119f;
   // a / 127 correctly rounded: a first quotient and one step with its exact
   // remainder (Markstein's division; checked against a / 127 for every mantissa)
   constexpr float kInv = 1.0f / 127.0f;
   const float q = a * kInv;
   scale = fmaf(fmaf(-127.0f, q, a), kInv, q);
-  // 127 a stays finite, and its reciprocal normal, with a large a scaled down
-  const float down = a > 0x1p100f ? 0x1p-8f : 1.0f;
+  scale = bad ? __uint_as_float(0x7FC00000u) : (none ? 0.f : scale);
+  // a large a is scaled down, so that its reciprocal stays normal
+  constexpr float kTop = sizeof(E) == 2 ? 127.0f * (1.0f + 0x1p-19f) : 127.0f;
+  const bool large = a > 0x1p100f;
   float inv;
-  asm("rcp.approx.f32 %0, %1;" : "=f"(inv) : "f"(a * down));
-  inv = inv * 127.0f * down;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(large ? a * 0x1p-8f : a));
+  inv *= large ? kTop * 0x1p-8f : kTop;
   constexpr float kMagic = 12582912.0f;
-  uint32_t w[8];
-  float border = 0.f;
-  Vals y, z;
+  Vals z;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    y.p[i] = __fmul2_rn(v.p[i], both(inv));
-    z.p[i] = __fadd2_rn(y.p[i], both(kMagic));
-    const float2 d = __ffma2_rn(__fadd2_rn(z.p[i], both(-kMagic)), both(-1.f), y.p[i]);
-    border = fmaxf(border, fmaxf(fabsf(d.x), fabsf(d.y)));
+  for (int i = 0; i < 4; ++i) z.p[i] = __ffma2_rn(v.p[i], both(inv), both(kMagic));
+  bool close;
+  if constexpr (sizeof(E) == 2) {
+    close = (m & 0x007F0000u) == 0x007E0000u;
+  } else {
+    float border = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 d =
+          __ffma2_rn(v.p[i], both(inv), __ffma2_rn(z.p[i], both(-1.f), both(kMagic)));
+      border = max_abs3(border, d.x, d.y);
+    }
+    close = border > 0.5f - 0x1p-14f;
   }
-  if (border > 0.5f - 0x1p-14f) {
+  if (close) {
+    const float down = large ? 0x1p-8f : 1.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float c = z.at(i) - kMagic;
-      z.at(i) = settle(v.at(i) * down, a * down, c, y.at(i) - c) + kMagic;
+      z.at(i) = settle(v.at(i) * down, a * down, c, fmaf(v.at(i), inv, -c)) + kMagic;
     }
   }
+  uint32_t w[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(z.at(i));
   const uint32_t lo = __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040),
                                   0x5410);
   const uint32_t hi = __byte_perm(__byte_perm(w[4], w[5], 0x0040), __byte_perm(w[6], w[7], 0x0040),
                                   0x5410);
-  return make_uint2(lo, hi);
+  return bad || none ? make_uint2(0u, 0u) : make_uint2(lo, hi);
 }
 
 // code * scale of eight codes, exact integers times the fp32 scale (one
