@@ -45,44 +45,55 @@ struct Walk {
   long long kv_head;               // elements between heads of k and v
 };
 
-// One row of q, k and v on its way through shared memory.
-template <typename E, int D, bool From8>
+// Two rows of q, k and v on their way through shared memory.
+template <typename E, int D, bool From8, bool TwoHeads>
 struct Feed {
-  static constexpr int kSlot = Slot<E, D>::kBytes, kBytes = 3 * kSlot;
+  static constexpr int kSlot = Slot<E, D>::kBytes, kBytes = 6 * kSlot;
   __device__ __forceinline__ static void ask(char* s, const Walk& w, const NormRopeArgs& a, int n,
-                                             int h, int lane, int l) {
+                                             int h, int u, int sub, int l) {
 #pragma unroll
     for (int i = 0; i < 3; ++i)
-      Slot<E, D>::ask(s + i * kSlot, at_bytes(static_cast<const E*>(a.in[i]) + h * D, n, w.ld),
-                      lane, l);
+      Slot<E, D>::ask(s + (3 * u + i) * kSlot,
+                      at_bytes(static_cast<const E*>(a.in[i]) + h * D, n, w.ld),
+                      sub * (D / 8) + l, l);
   }
-  __device__ __forceinline__ static Raw<E> raw(const char* s, int i, int lane) {
-    return Slot<E, D>::get(s + i * kSlot, lane);
+  __device__ __forceinline__ static Raw<E> raw(const char* s, int i, int u, int sub, int l) {
+    return Slot<E, D>::get(s + (3 * u + i) * kSlot, sub * (D / 8) + l);
   }
-  __device__ __forceinline__ static Vals get(const char* s, int i, int lane) {
-    return unpack(raw(s, i, lane));
+  // x r of q and k of both rows
+  __device__ __forceinline__ static void load(const char* s, float eps, int sub, int l,
+                                              Vals (&x)[4]) {
+    float r[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = unpack(raw(s, k & 1, k / 2, sub, l));
+    normalise<D>(x, eps, l, r);
   }
-  __device__ __forceinline__ static Raw<E> value(const char* s, int lane) {
-    return raw(s, 2, lane);
+  __device__ __forceinline__ static Raw<E> value(const char* s, int u, int sub, int l) {
+    return raw(s, 2, u, sub, l);
   }
 };
-template <typename E, int D>
-struct Feed<E, D, true> {
-  static constexpr int kSlot = Slot8<E, D>::kBytes, kBytes = 3 * kSlot;
+template <typename E, int D, bool TwoHeads>
+struct Feed<E, D, true, TwoHeads> {
+  using C = CodeRows<E, D, 3, TwoHeads>;
+  static constexpr int kBytes = C::kBytes;
   __device__ __forceinline__ static void ask(char* s, const Walk& w, const NormRopeArgs& a, int n,
-                                             int h, int lane, int l) {
+                                             int h, int u, int sub, int l) {
+    C::ask(s, a.codes, a.scales, n, h, w.n_h, u, sub, l);
+  }
+  __device__ __forceinline__ static void load(const char* s, float eps, int sub, int l,
+                                              Vals (&x)[4]) {
+    uint2 c[4];
+    float sc[4], r[4];
 #pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      const uint32_t row = (uint32_t)((n * 3 + i) * w.n_h + h);
-      Slot8<E, D>::ask(s + i * kSlot, at_bytes(a.codes, row, D), a.scales + row, lane, l);
+    for (int k = 0; k < 4; ++k) {
+      c[k] = C::codes(s, k & 1, k / 2, sub, l);
+      sc[k] = C::scale(s, k & 1, k / 2, sub);
     }
+    normalise<D>(c, sc, eps, l, x, r);
   }
-  __device__ __forceinline__ static Vals get(const char* s, int i, int lane) {
-    return decode8(Slot8<E, D>::codes(s + i * kSlot, lane), Slot8<E, D>::scale(s + i * kSlot, lane));
-  }
-  __device__ __forceinline__ static Raw<E> value(const char* s, int lane) {
+  __device__ __forceinline__ static Raw<E> value(const char* s, int u, int sub, int l) {
     Raw<E> r;
-    pack(get(s, 2, lane), r);
+    pack(decode8(C::codes(s, 2, u, sub, l), C::scale(s, 2, u, sub)), r);
     return r;
   }
 };
@@ -98,7 +109,7 @@ template <typename E, int D, bool From8, bool TwoHeads>
 struct Smem {
   static constexpr int kNA = TwoHeads ? 2 : 1;
   static constexpr int kLanes = kWarps * (D / 8);
-  static constexpr int kRing = stages<E, From8>() * kWarps * 2 * Feed<E, D, From8>::kBytes;
+  static constexpr int kRing = stages<E, From8>() * kWarps * Feed<E, D, From8, TwoHeads>::kBytes;
   static constexpr int kSpots = stages<E, From8>() * kWarps * 8 * (int)sizeof(Spot);
   static constexpr int kTotal = kMaxUp * kNA * D * (int)sizeof(double);
   static constexpr int kBytes = kRing + kSpots + kTotal + kNA * 8 * kLanes * (int)sizeof(double);
@@ -109,11 +120,11 @@ __global__ void __launch_bounds__(kThreads, 2)
 k_norm_rope(const __grid_constant__ Walk w, const __grid_constant__ NormRopeArgs a,
             const __grid_constant__ NormRopeOut o) {
   constexpr int G = D / 8, R = 32 / G, NA = TwoHeads ? 2 : 1;
-  using F = Feed<E, D, From8>;
+  using F = Feed<E, D, From8, TwoHeads>;
   using M = Smem<E, D, From8, TwoHeads>;
   constexpr int S = stages<E, From8>();
   extern __shared__ __align__(16) char smem[];
-  char* ring = smem + (threadIdx.x >> 5) * (S * 2 * F::kBytes);
+  char* ring = smem + (threadIdx.x >> 5) * (S * F::kBytes);
   Spot* spots = reinterpret_cast<Spot*>(smem + M::kRing) + (threadIdx.x >> 5) * (S * 8);
   double* total = reinterpret_cast<double*>(smem + M::kRing + M::kSpots);
   double(&sums)[NA][8][M::kLanes] =
@@ -170,7 +181,7 @@ k_norm_rope(const __grid_constant__ Walk w, const __grid_constant__ NormRopeArgs
           n = spot.n;
           if (l == 0) spots[stage * 8 + u * 4 + sub] = spot;
         }
-        F::ask(ring + (stage * 2 + u) * F::kBytes, w, a, n, h0 + (TwoHeads ? u : 0), lane, l);
+        F::ask(ring + stage * F::kBytes, w, a, n, h0 + (TwoHeads ? u : 0), u, sub, l);
       }
     }
     fetch_commit();
@@ -198,24 +209,19 @@ k_norm_rope(const __grid_constant__ Walk w, const __grid_constant__ NormRopeArgs
       }
     }
     fetch_wait<S - 1>();
-    const char* in[2] = {ring + stage * 2 * F::kBytes, ring + (stage * 2 + 1) * F::kBytes};
+    if constexpr (From8) __syncwarp();
+    const char* in = ring + stage * F::kBytes;
     stage = stage == S - 1 ? 0 : stage + 1;
-    Vals x[4] = {F::get(in[0], 0, lane), F::get(in[0], 1, lane), F::get(in[1], 0, lane),
-                 F::get(in[1], 1, lane)};
     if constexpr (To8) {
-      const Raw<E> raw[6] = {F::raw(in[0], 0, lane), F::raw(in[0], 1, lane),
-                             F::raw(in[0], 2, lane), F::raw(in[1], 0, lane),
-                             F::raw(in[1], 1, lane), F::raw(in[1], 2, lane)};
-      uint32_t m[6];
-#pragma unroll
-      for (int i = 0; i < 3; ++i) group_max<G>(raw[i], raw[i + 3], m[i], m[i + 3]);
 #pragma unroll
       for (int i = 0; i < 3; ++i) {
+        const Raw<E> raw[2] = {F::raw(in, i, 0, sub, l), F::raw(in, i, 1, sub, l)};
+        uint32_t m[2];
         float sc[2];
         uint2 c[2];
+        group_max<G>(raw[0], raw[1], m[0], m[1]);
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-          c[u] = encode8<E>(i < 2 ? x[2 * u + i] : unpack(raw[2 + 3 * u]), m[i + 3 * u], sc[u]);
+        for (int u = 0; u < 2; ++u) c[u] = encode8<E>(unpack(raw[u]), m[u], sc[u]);
         const uint32_t row[2] = {(uint32_t)((n[0] * 3 + i) * w.n_h + h0),
                                  (uint32_t)((n[1] * 3 + i) * w.n_h + h0 + (TwoHeads ? 1 : 0))};
 #pragma unroll
@@ -232,15 +238,15 @@ k_norm_rope(const __grid_constant__ Walk w, const __grid_constant__ NormRopeArgs
         }
       }
     }
-    float rms[4], pre[4];
-    inv_rms<D>(x, a.eps, l, rms, pre);
+    Vals x[4];
+    F::load(in, a.eps, sub, l, x);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       Vals &q = x[2 * u], &k = x[2 * u + 1];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        q.p[i] = __fmul2_rn(__fmul2_rn(q.p[i], both(rms[2 * u])), gq.p[i]);
-        k.p[i] = __fmul2_rn(__fmul2_rn(k.p[i], both(rms[2 * u + 1])), gk.p[i]);
+        q.p[i] = __fmul2_rn(q.p[i], gq.p[i]);
+        k.p[i] = __fmul2_rn(k.p[i], gk.p[i]);
       }
       turn(q, cs[TwoHeads ? 0 : u]);
       turn(k, cs[TwoHeads ? 0 : u]);
@@ -253,7 +259,7 @@ k_norm_rope(const __grid_constant__ Walk w, const __grid_constant__ NormRopeArgs
         const int p = j * w.L + r[u];
         store_raw<D>(at_bytes(static_cast<E*>(o.k) + h * w.kv_head, p, w.kv_tok), l, s);
         store_raw<D>(at_bytes(static_cast<E*>(o.v) + h * w.kv_head, p, w.kv_tok), l,
-                     F::value(in[u], lane));
+                     F::value(in, u, sub, l));
         Vals& to = acc[TwoHeads ? u : 0];
 #pragma unroll
         for (int i = 0; i < 4; ++i) to.p[i] = __fadd2_rn(to.p[i], k.p[i]);

@@ -34,28 +34,44 @@ struct Walk {
   int n_items, n_chunks;
 };
 
-// The gradients and the raw q and k of one row on their way through shared
+// The gradients and the raw q and k of two rows on their way through shared
 // memory.
-template <typename E, int D, bool From8>
+template <typename E, int D, bool From8, bool TwoHeads>
 struct Feed {
-  static constexpr int kSlot = Slot<E, D>::kBytes;
-  static constexpr int kRaw = From8 ? Slot8<E, D>::kBytes : kSlot;
-  static constexpr int kBytes = 3 * kSlot + 2 * kRaw;
-  __device__ __forceinline__ static Vals raw(const char* s, int i, int lane) {
-    s += 3 * kSlot + i * kRaw;
-    if constexpr (From8)
-      return decode8(Slot8<E, D>::codes(s, lane), Slot8<E, D>::scale(s, lane));
-    else
-      return unpack(Slot<E, D>::get(s, lane));
+  using C = CodeRows<E, D, 2, TwoHeads>;
+  static constexpr int kSlot = Slot<E, D>::kBytes, kRaw = 6 * kSlot;
+  static constexpr int kBytes = kRaw + (From8 ? C::kBytes : 4 * kSlot);
+  __device__ __forceinline__ static Raw<E> grad(const char* s, int i, int u, int lane) {
+    return Slot<E, D>::get(s + (3 * u + i) * kSlot, lane);
+  }
+  // x r of q and k of both rows, and r
+  __device__ __forceinline__ static void load(const char* s, float eps, int sub, int l,
+                                              Vals (&x)[4], float (&r)[4]) {
+    s += kRaw;
+    if constexpr (From8) {
+      uint2 c[4];
+      float sc[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        c[k] = C::codes(s, k & 1, k / 2, sub, l);
+        sc[k] = C::scale(s, k & 1, k / 2, sub);
+      }
+      normalise<D>(c, sc, eps, l, x, r);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        x[k] = unpack(Slot<E, D>::get(s + k * kSlot, sub * (D / 8) + l));
+      normalise<D>(x, eps, l, r);
+    }
   }
 };
 
 // Iterations a warp's loads run ahead.
 constexpr int kStages = 2;
 
-template <typename E, int D, bool From8>
+template <typename E, int D, bool From8, bool TwoHeads>
 struct Smem {
-  static constexpr int kRing = kStages * kWarps * 2 * Feed<E, D, From8>::kBytes;
+  static constexpr int kRing = kStages * kWarps * Feed<E, D, From8, TwoHeads>::kBytes;
   static constexpr int kSpots = kStages * kWarps * 8 * (int)sizeof(Spot);
   static constexpr int kLanes = kWarps * (D / 8);      // lanes of one row in every warp
   static constexpr int kBytes = kRing + kSpots + 16 * kLanes * (int)sizeof(double);
@@ -68,12 +84,12 @@ k_norm_rope_bwd(const __grid_constant__ Walk w, const __grid_constant__ NormRope
                 E* __restrict__ oq, E* __restrict__ ok, E* __restrict__ ov, float* part) {
   constexpr int G = D / 8, R = 32 / G, S = kStages;
   constexpr int kStep = kWarps * R, kStride = kStep * (TwoHeads ? 1 : 2);
-  using F = Feed<E, D, From8>;
-  using M = Smem<E, D, From8>;
+  using F = Feed<E, D, From8, TwoHeads>;
+  using M = Smem<E, D, From8, TwoHeads>;
   extern __shared__ __align__(16) char smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane / G, l = lane % G;
-  char* ring = smem + warp * (S * 2 * F::kBytes);
+  char* ring = smem + warp * (S * F::kBytes);
   Spot* spots = reinterpret_cast<Spot*>(smem + M::kRing) + warp * (S * 8);
   double(&sums)[16][M::kLanes] =
       *reinterpret_cast<double(*)[16][M::kLanes]>(smem + M::kRing + M::kSpots);
@@ -122,20 +138,18 @@ k_norm_rope_bwd(const __grid_constant__ Walk w, const __grid_constant__ NormRope
           }
         }
         const int h = ahead.h0 + (TwoHeads ? u : 0);
-        char* to = ring + (stage * 2 + u) * F::kBytes;
-        Slot<E, D>::ask(to, at_bytes(dq + h * D, n, row3), lane, l);
-        Slot<E, D>::ask(to + F::kSlot, at_bytes(dk + h * D, n, row3), lane, l);
-        Slot<E, D>::ask(to + 2 * F::kSlot, at_bytes(dv + h * D, n, row3), lane, l);
-        to += 3 * F::kSlot;
+        char* to = ring + stage * F::kBytes;
+        Slot<E, D>::ask(to + 3 * u * F::kSlot, at_bytes(dq + h * D, n, row3), lane, l);
+        Slot<E, D>::ask(to + (3 * u + 1) * F::kSlot, at_bytes(dk + h * D, n, row3), lane, l);
+        Slot<E, D>::ask(to + (3 * u + 2) * F::kSlot, at_bytes(dv + h * D, n, row3), lane, l);
+        to += F::kRaw;
         if constexpr (From8) {
-          const uint32_t row = (uint32_t)(n * 3 * w.n_h + h);
-          Slot8<E, D>::ask(to, at_bytes(a.codes, row, D), a.scales + row, lane, l);
-          Slot8<E, D>::ask(to + F::kRaw, at_bytes(a.codes, row + w.n_h, D),
-                           a.scales + row + w.n_h, lane, l);
+          F::C::ask(to, a.codes, a.scales, n, h, w.n_h, u, sub, l);
         } else {
-          Slot<E, D>::ask(to, at_bytes(static_cast<const E*>(a.in[0]) + h * D, n, w.ld), lane, l);
-          Slot<E, D>::ask(to + F::kRaw, at_bytes(static_cast<const E*>(a.in[1]) + h * D, n, w.ld),
-                          lane, l);
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            Slot<E, D>::ask(to + (2 * u + i) * F::kSlot,
+                            at_bytes(static_cast<const E*>(a.in[i]) + h * D, n, w.ld), lane, l);
         }
       }
       ahead.n0 += kStride;
@@ -171,28 +185,25 @@ k_norm_rope_bwd(const __grid_constant__ Walk w, const __grid_constant__ NormRope
       }
       const int h0 = cur.h0;
       fetch_wait<S - 1>();
-      const char* in[2] = {ring + stage * 2 * F::kBytes, ring + (stage * 2 + 1) * F::kBytes};
+      if constexpr (From8) __syncwarp();
+      const char* in = ring + stage * F::kBytes;
       stage = stage == S - 1 ? 0 : stage + 1;
-      Vals x[4];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        x[2 * u] = F::raw(in[u], 0, lane);
-        x[2 * u + 1] = F::raw(in[u], 1, lane);
+      for (int u = 0; u < 2; ++u)
         if (mine[u])
           store_raw<D>(at_bytes(ov + (h0 + (TwoHeads ? u : 0)) * D, n[u], w.ld_out), l,
-                       Slot<E, D>::get(in[u] + 2 * F::kSlot, lane));
-      }
-      float r[4], pre[4], dot[4];
-      inv_rms<D>(x, a.eps, l, r, pre);
+                       F::grad(in, 2, u, lane));
+      Vals x[4];
+      float r[4], dot[4];
+      F::load(in, a.eps, sub, l, x, r);          // xh = x r
       Vals g[4];                                // the gradients, then w = u g
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        g[k] = unpack(Slot<E, D>::get(in[k / 2] + (k & 1) * F::kSlot, lane));
+        g[k] = unpack(F::grad(in, k & 1, k / 2, lane));
         turn_back(g[k], cs[TwoHeads ? 0 : k / 2]);
         Vals& sum = k & 1 ? wk : wq;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          x[k].p[i] = __fmul2_rn(x[k].p[i], both(r[k]));                // xh
           if (mine[k / 2]) sum.p[i] = __ffma2_rn(g[k].p[i], x[k].p[i], sum.p[i]);
           g[k].p[i] = __fmul2_rn(g[k].p[i], k & 1 ? gk.p[i] : gq.p[i]);
         }
@@ -201,10 +212,9 @@ k_norm_rope_bwd(const __grid_constant__ Walk w, const __grid_constant__ NormRope
       spread<G>(quarter_sums<G>(dot, l) * (-1.0f / D), dot);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float rr = r[k] * pre[k];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          g[k].p[i] = __fmul2_rn(__ffma2_rn(x[k].p[i], both(dot[k]), g[k].p[i]), both(rr));
+          g[k].p[i] = __fmul2_rn(__ffma2_rn(x[k].p[i], both(dot[k]), g[k].p[i]), both(r[k]));
         if (mine[k / 2]) {
           Raw<E> s;
           pack(g[k], s);
@@ -279,7 +289,7 @@ cudaError_t launch_t(const Prob& P, const NormRopeArgs& a, const void* dq, const
   const int ctas = min(w.n_items, slots);
   float* part = dweight ? static_cast<float*>(ws) : nullptr;
   const auto kernel = k_norm_rope_bwd<E, D, From8, TwoHeads>;
-  constexpr int smem = Smem<E, D, From8>::kBytes;
+  constexpr int smem = Smem<E, D, From8, TwoHeads>::kBytes;
   static SmemOptIn opt_in;
   if (const cudaError_t e = opt_in.set(kernel, smem); e != cudaSuccess) return e;
   {

@@ -123,25 +123,44 @@ struct Slot {
   }
 };
 
-// The same for rows of codes with their scale.
-template <typename E, int D>
-struct Slot8 {
-  static constexpr int kBytes = 32 * 12;
-  __device__ __forceinline__ static void ask(char* s, const int8_t* codes, const float* scale,
-                                             int lane, int l) {
-    if constexpr (sizeof(E) == 2) {
-      fetch<8>(s + lane * 8, codes + l * 8);
-    } else {
-      fetch<4>(s + lane * 8, codes + l * 4);
-      fetch<4>(s + lane * 8 + 4, codes + D / 2 + l * 4);
+// T rows of codes (raw q, k and, if T = 3, v of a token and head) and their
+// scales, of two neighbouring heads of R tokens or of one head of two times R.
+// Two heads' codes of a token are neighbours, so sixteen of them are one copy
+// and a lane reads what others asked for: a __syncwarp stands between its
+// wait and its reads, and between those and the next copies.
+template <typename E, int D, int T, bool TwoHeads>
+struct CodeRows {
+  static constexpr int G = D / 8, R = 32 / G;
+  static constexpr int kScales = T * 512, kBytes = kScales + 2 * R * T * 4;
+  __device__ __forceinline__ static void ask(char* s, const int8_t* codes, const float* scales,
+                                             int n, int h, int n_h, int u, int sub, int l) {
+    if (TwoHeads && u == 1) return;
+#pragma unroll
+    for (int i = 0; i < T; ++i) {
+      const int8_t* row = at_bytes(codes, (n * 3 + i) * n_h + h, D);
+      if constexpr (TwoHeads)
+        fetch<16>(s + i * 512 + (sub * G + l) * 16, row + l * 16);
+      else
+        fetch<8>(s + i * 512 + u * 256 + (sub * G + l) * 8, row + l * 8);
     }
-    fetch<4>(s + 256 + lane * 4, scale);
+    if (l < T) {
+      const float* from = scales + (uint32_t)((n * 3 + l) * n_h + h);
+      float* to = reinterpret_cast<float*>(s + kScales);
+      if constexpr (TwoHeads)
+        fetch<8>(to + (sub * T + l) * 2, from);
+      else
+        fetch<4>(to + (u * R + sub) * T + l, from);
+    }
   }
-  __device__ __forceinline__ static uint2 codes(const char* s, int lane) {
-    return *reinterpret_cast<const uint2*>(s + lane * 8);
+  __device__ __forceinline__ static uint2 codes(const char* s, int i, int u, int sub, int l) {
+    s += i * 512 + (TwoHeads ? (sub * 2 + u) * D : u * 256 + sub * D);
+    if constexpr (sizeof(E) == 2) return reinterpret_cast<const uint2*>(s)[l];
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(s);
+    return make_uint2(p[l], p[D / 8 + l]);
   }
-  __device__ __forceinline__ static float scale(const char* s, int lane) {
-    return *reinterpret_cast<const float*>(s + 256 + lane * 4);
+  __device__ __forceinline__ static float scale(const char* s, int i, int u, int sub) {
+    const float* p = reinterpret_cast<const float*>(s + kScales);
+    return TwoHeads ? p[(sub * T + i) * 2 + u] : p[(u * R + sub) * T + i];
   }
 };
 
@@ -369,27 +388,30 @@ __device__ __forceinline__ uint2 encode8(const Vals& v, uint32_t m, float& scale
   return bad || none ? make_uint2(0u, 0u) : make_uint2(lo, hi);
 }
 
-// code * scale of eight codes, exact integers times the fp32 scale (one
-// rounding).  A byte c + 128 in the mantissa of 2^23 is 2^23 + 128 + c.
-__device__ __forceinline__ Vals decode8(uint2 c, float scale) {
+// Eight codes as fp32.  A byte c + 128 in the mantissa of 2^23 is 2^23 + 128 + c.
+__device__ __forceinline__ Vals code_values(uint2 c) {
   const uint32_t w[2] = {c.x ^ 0x80808080u, c.y ^ 0x80808080u};
   Vals v;
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     v.at(i) = __uint_as_float(__byte_perm(w[i >> 2], 0x4B000000u, 0x7440 + (i & 3)));
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    v.p[i] = __fmul2_rn(__fadd2_rn(v.p[i], both(-8388736.0f)), both(scale));
+  for (int i = 0; i < 4; ++i) v.p[i] = __fadd2_rn(v.p[i], both(-8388736.0f));
   return v;
 }
 
-// A lane's eight codes of a row of D codes, in the element order of E.
-template <typename E, int D>
-__device__ __forceinline__ uint2 load_codes(const int8_t* row, int l) {
-  if (sizeof(E) == 2) return __ldg(reinterpret_cast<const uint2*>(row) + l);
-  const uint32_t* p = reinterpret_cast<const uint32_t*>(row);
-  return make_uint2(__ldg(p + l), __ldg(p + D / 8 + l));
+__device__ __forceinline__ Vals scaled(Vals v, float by) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v.p[i] = __fmul2_rn(v.p[i], both(by));
+  return v;
 }
+
+// code * scale, one rounding.
+__device__ __forceinline__ Vals decode8(uint2 c, float scale) {
+  return scaled(code_values(c), scale);
+}
+
+// A lane's eight codes into a row of D codes, from the element order of E.
 template <typename E, int D>
 __device__ __forceinline__ void store_codes(int8_t* row, int l, uint2 c) {
   if (sizeof(E) == 2) {
@@ -441,6 +463,49 @@ __device__ __forceinline__ void inv_rms(Vals (&x)[N], float eps, int l, float (&
       const float again = row_sum<G>(lane_dot(x[k], x[k]));
       if (big) r[k] = rsqrt_normal(again * (1.0f / D));
     }
+  }
+}
+
+// x r of four rows (and r) from raw values: x becomes x r.
+template <int D>
+__device__ __forceinline__ void normalise(Vals (&x)[4], float eps, int l, float (&r)[4]) {
+  float pre[4];
+  inv_rms<D>(x, eps, l, r, pre);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    x[k] = scaled(x[k], r[k]);
+    r[k] *= pre[k];
+  }
+}
+
+// The same from codes, without their scales s where these are ordinary:
+// x r = c / sqrt(mean c^2 + eps / s^2), the sum of squared codes an exact
+// integer.  Where eps / s^2 is huge (or s is zero or NaN) the values are formed.
+template <int D>
+__device__ __forceinline__ void normalise(const uint2 (&c)[4], const float (&s)[4], float eps,
+                                          int l, Vals (&x)[4], float (&r)[4]) {
+  constexpr int G = D / 8;
+  float ss[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    ss[k] = (float)__dp4a((int)c[k].x, (int)c[k].x, __dp4a((int)c[k].y, (int)c[k].y, 0));
+  const bool hi = l & (G / 2), hi2 = l & (G / 4);
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;"
+      : "=f"(inv) : "f"(hi ? (hi2 ? s[3] : s[2]) : (hi2 ? s[1] : s[0])));
+  const float e = eps * inv * inv;
+  const float sum = quarter_sums<G>(ss, l);
+  if (!__any_sync(kAll, !(e < 0x1p100f))) {
+    const float rc = rsqrt_normal(fmaf(sum, 1.0f / D, e));
+    float rx[4];
+    spread<G>(rc, rx);
+    spread<G>(rc * inv, r);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = scaled(code_values(c[k]), rx[k]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = decode8(c[k], s[k]);
+    normalise<D>(x, eps, l, r);
   }
 }
 
