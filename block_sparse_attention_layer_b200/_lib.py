@@ -74,14 +74,18 @@ class LayerShape:
     def s(self) -> int:
         return self.T * self.H * self.W
 
+    # what calls on this shape need each time, built once (the fields are frozen)
+
     @functools.cached_property
     def _ref(self):
-        """The shape as the ABI takes it, built once (the fields are frozen)."""
         return ctypes.byref(self.c())
 
     @functools.cached_property
-    def _blocks(self) -> int:
-        return num_blocks(self)
+    def _sizes(self):
+        """(shapes of token-order rows, partition-order rows, raw rows, block
+        means, torch dtype)."""
+        s, h, d = self.s, self.n_heads, self.head_dim
+        return (s, h, d), (h, s, d), (s, 3, h, d), (h, num_blocks(self), d), _torch_dtype(self)
 
     def c(self) -> CShape:
         return CShape(self.T, self.H, self.W, self.n_heads, self.head_dim, self.mode,
@@ -323,283 +327,6 @@ def attn_bwd(shape, q, k_perm, v_perm, sel_bits, ws, scale, lse, dout, dq, dk, d
         ws.numel() * ws.element_size(), float(scale), _ptr(lse), _ptr(dout),
         _ptr(dq), _ptr(dk), _ptr(dv), _ptr(ws_bwd), ws_bwd.numel() * ws_bwd.element_size(),
         _stream(stream)))
-
-
-# ------------------------------------ norm + rotation, 8-bit checkpoints
-
-@dataclass(frozen=True, eq=False)
-class NormRope:
-    """Norm and rotation of a layer's queries and keys (include/vmoba.h:
-    vmoba_norm_rope).  q_weight, k_weight: fp32 CUDA tensors [head_dim], or
-    None for ones; table: from rope_table, or None if no pair turns; dims:
-    how many of a head's dimensions turn with t, y and x."""
-    q_weight: object = None
-    k_weight: object = None
-    eps: float = 1e-6
-    table: object = None
-    dims: tuple = (0, 0, 0)
-
-
-@dataclass(frozen=True, eq=False)
-class Act8:
-    """An 8-bit activation checkpoint: int8 codes of the activation's shape and
-    one fp32 scale for each group of neighbouring values of the last axis."""
-    codes: object
-    scales: object
-    group: int
-
-    @classmethod
-    def empty(cls, shape, group: int, device="cuda") -> "Act8":
-        import torch
-        if group not in (64, 128):
-            raise ValueError("group: expected 64 or 128")
-        shape = tuple(shape)
-        n = -(-shape[-1] // group)
-        return cls(torch.empty(shape, dtype=torch.int8, device=device),
-                   torch.empty(shape[:-1] + (n,), dtype=torch.float32, device=device), group)
-
-
-def rope_dims(head_dim: int) -> tuple:
-    """The usual split of a head's dimensions over (t, y, x): two of six parts
-    of the pairs each for y and x, the rest for t (44, 42, 42 of 128)."""
-    hw = 2 * (head_dim // 6)
-    return head_dim - 2 * hw, hw, hw
-
-
-def _table_rows(shape: LayerShape, dims) -> int:
-    return (shape.T * dims[0] + shape.H * dims[1] + shape.W * dims[2]) // 2
-
-
-class _Call:
-    """Checks the tensors of one call and hands out their addresses: every one
-    a CUDA tensor on the same device, which is current during the call."""
-
-    __slots__ = ("name", "device")
-
-    def __init__(self, name: str):
-        self.name = name
-        self.device = -2            # a host tensor's is -1
-
-    def addr(self, t, shape, dtype, name, strided=False) -> int:
-        if t.shape != shape:
-            raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-        if t.dtype is not dtype:
-            raise ValueError(f"{name}: expected dtype {dtype}, got {t.dtype}")
-        device = t.get_device()
-        if device != self.device:
-            if not t.is_cuda:
-                raise ValueError(f"{name}: expected a CUDA tensor")
-            if self.device >= 0:
-                raise ValueError(f"{name}: expected a tensor on cuda:{self.device}, got {t.device}")
-            self.device = device
-        if not strided and not t.is_contiguous():
-            raise ValueError(f"{name}: expected a contiguous tensor")
-        return t.data_ptr()
-
-    def raw(self, shape: LayerShape, x, dtype, name):
-        """(q, k, v addresses, token stride) of raw rows: a [s][3][heads][d]
-        tensor or three [s][heads][d] ones, the last two axes dense."""
-        s, h, d = shape.s, shape.n_heads, shape.head_dim
-        if isinstance(x, (tuple, list)):
-            if len(x) != 3:
-                raise ValueError(f"{name}: expected one tensor or three")
-            at = [self.addr(t, (s, h, d), dtype, name, True) for t in x]
-            ld = self.stride(x[0], h * d, (d, 1), name)
-            for t in x[1:]:
-                if self.stride(t, h * d, (d, 1), name) != ld:
-                    raise ValueError(f"{name}: expected one token stride, got "
-                                     f"{[t.stride(0) for t in x]}")
-            return at, ld
-        p, step = self.addr(x, (s, 3, h, d), dtype, name, True), h * d * x.element_size()
-        return (p, p + step, p + 2 * step), self.stride(x, 3 * h * d, (h * d, d, 1), name)
-
-    @staticmethod
-    def stride(t, least, dense, name) -> int:
-        """The token stride of rows whose other axes are dense."""
-        st = t.stride()
-        if st[1:] != dense and any(n > 1 and have != want
-                                   for n, have, want in zip(t.shape[1:], st[1:], dense)):
-            raise ValueError(f"{name}: expected dense rows, got strides {tuple(st)}")
-        if t.shape[0] == 1:
-            return least
-        if st[0] < least:
-            raise ValueError(f"{name}: rows overlap, strides {tuple(st)}")
-        return st[0]
-
-    def norm(self, shape: LayerShape, nr: NormRope) -> CNormRope:
-        import torch
-        try:
-            dt, dh, dw = nr.dims
-        except (TypeError, ValueError):
-            dt = dh = dw = -1
-        if dt < 0 or dh < 0 or dw < 0 or (dt | dh | dw) & 1 or dt + dh + dw > shape.head_dim:
-            raise ValueError(f"dims: expected three even numbers >= 0 of sum <= "
-                             f"{shape.head_dim}, got {nr.dims}")
-        gq, gk, table, d = nr.q_weight, nr.k_weight, 0, (shape.head_dim,)
-        if gq is not None:
-            gq = self.addr(gq, d, torch.float32, "q_weight")
-        if gk is not None:
-            gk = self.addr(gk, d, torch.float32, "k_weight")
-        if dt + dh + dw:
-            if nr.table is None:
-                raise ValueError("table: expected a rotation table (rope_table)")
-            table = self.addr(nr.table, (_table_rows(shape, nr.dims), 2), torch.float32, "table")
-        return CNormRope(gq, gk, nr.eps, table, dt, dh, dw)
-
-    def ckpt(self, c: Act8, shape, group, name):
-        import torch
-        if c.group != group:
-            raise ValueError(f"{name}: expected groups of {group}, got {c.group}")
-        return (self.addr(c.codes, shape, torch.int8, name + ".codes"),
-                self.addr(c.scales, (*shape[:-1], -(-shape[-1] // group)), torch.float32,
-                          name + ".scales"))
-
-    def run(self, stream, *args) -> None:
-        import torch
-        device = self.device
-        if stream is None:
-            stream = torch._C._cuda_getCurrentRawStream(device)
-        elif stream.device.index != device:
-            raise ValueError(f"stream: expected one of cuda:{device}, got {stream.device}")
-        else:
-            stream = stream.cuda_stream
-        fn = getattr(_LIB or lib(), self.name)
-        if device == torch._C._cuda_getDevice():
-            rc = fn(*args, stream)
-        else:
-            with torch.cuda.device(device):
-                rc = fn(*args, stream)
-        if rc:
-            _check(self.name, rc)
-
-
-def rope_table(shape: LayerShape, dims, base: float = 10000.0, origin=(0, 0, 0), device="cuda",
-               stream=None):
-    """The rotation table of the shape's grid: (cos, sin) of each position and
-    pair of the three axes, [T dims[0]/2 + H dims[1]/2 + W dims[2]/2][2] fp32,
-    positions counted from ``origin`` (a chunk of a longer video)."""
-    import torch
-    dims = tuple(int(n) for n in dims)
-    table = torch.empty((max(_table_rows(shape, dims), 0), 2), dtype=torch.float32, device=device)
-    c = _Call("vmoba_rope_table")
-    at = c.addr(table, table.shape, torch.float32, "table")
-    c.run(stream, shape._ref, *dims, float(base), *(int(o) for o in origin), at)
-    return table
-
-
-def _norm_rope_fwd(name, shape, nr, qkv, outs, ckpt, stream):
-    dt = _torch_dtype(shape)
-    s, h, d = shape.s, shape.n_heads, shape.head_dim
-    if isinstance(qkv, Act8):
-        if ckpt is not None:
-            raise ValueError("ckpt: the raw values already come from a checkpoint")
-        c = _Call(name + "_act8")
-        src, more = c.ckpt(qkv, (s, 3, h, d), d, "qkv"), ()
-    else:
-        c = _Call(name)
-        at, ld = c.raw(shape, qkv, dt, "qkv")
-        src = (*at, ld)
-        more = (0, 0) if ckpt is None else c.ckpt(ckpt, (s, 3, h, d), d, "ckpt")
-    n = c.norm(shape, nr)
-    out = [c.addr(t, sz, ty or dt, what) for t, sz, ty, what in outs]
-    c.run(stream, shape._ref, ctypes.byref(n), *src, *out, *more)
-
-
-def qk_norm_rope(shape, nr, qkv, q, k, v, ckpt=None, stream=None):
-    """Norm of each head's query and key and their rotation, token order: raw
-    rows -> q, k, v [s][heads][d] (v is copied).  qkv: the projection's output
-    [s][3][heads][d] (tokens any stride apart), three [s][heads][d] tensors, or
-    an Act8 checkpoint of it; ckpt: an Act8 to store the raw rows in (groups
-    of head_dim), in the same pass."""
-    full = (shape.s, shape.n_heads, shape.head_dim)
-    _norm_rope_fwd("vmoba_qk_norm_rope", shape, nr, qkv,
-                   ((q, full, None, "q"), (k, full, None, "k"), (v, full, None, "v")), ckpt,
-                   stream)
-
-
-def qk_norm_rope_partition(shape, nr, qkv, q, k_perm, v_perm, blocks, ckpt=None, stream=None):
-    """As qk_norm_rope, into the sparse layer's buffers (in place of
-    partition): q in token order, k_perm, v_perm in partition order and the
-    fp32 means ``blocks`` of the rotated keys (before rounding to storage)."""
-    import torch
-    s, h, d = shape.s, shape.n_heads, shape.head_dim
-    _norm_rope_fwd("vmoba_qk_norm_rope_partition", shape, nr, qkv,
-                   ((q, (s, h, d), None, "q"), (k_perm, (h, s, d), None, "k_perm"),
-                    (v_perm, (h, s, d), None, "v_perm"),
-                    (blocks, (h, shape._blocks, d), torch.float32, "blocks")), ckpt, stream)
-
-
-def qk_norm_rope_bwd_workspace_size(shape: LayerShape) -> int:
-    return lib().vmoba_qk_norm_rope_bwd_workspace_size(shape._ref)
-
-
-def qk_norm_rope_bwd(shape, nr, qkv, dq, dk, dv, dqkv, dweight, ws, stream=None):
-    """Backward of qk_norm_rope and qk_norm_rope_partition: gradients of q, k, v
-    (token order) -> of the raw rows (dqkv, laid out like qkv) and of the two
-    norm weights (dweight [2][d] fp32, or None).  qkv: the forward's raw rows
-    or their Act8 checkpoint."""
-    import torch
-    dt = _torch_dtype(shape)
-    full = (shape.s, shape.n_heads, shape.head_dim)
-    if isinstance(qkv, Act8):
-        c = _Call("vmoba_qk_norm_rope_bwd_act8")
-        src = c.ckpt(qkv, (full[0], 3) + full[1:], full[2], "qkv")
-    else:
-        c = _Call("vmoba_qk_norm_rope_bwd")
-        at, ld = c.raw(shape, qkv, dt, "qkv")
-        src = (at[0], at[1], ld)
-    n = c.norm(shape, nr)
-    grads = [c.addr(t, full, dt, name) for name, t in (("dq", dq), ("dk", dk), ("dv", dv))]
-    out, ld_out = c.raw(shape, dqkv, dt, "dqkv")
-    dw = p_ws = n_ws = 0
-    if dweight is not None:
-        dw = c.addr(dweight, (2, full[2]), torch.float32, "dweight")
-        n_ws = ws.numel() * ws.element_size()
-        p_ws = c.addr(ws, ws.shape, ws.dtype, "ws")
-    c.run(stream, shape._ref, ctypes.byref(n), *src, *grads, *out, ld_out, dw, p_ws,
-          n_ws)
-
-
-def _act8_rows(t, name):
-    """(rows, cols, row stride) of a tensor whose leading axes are rows."""
-    if t.dim() < 2:
-        raise ValueError(f"{name}: expected at least two axes")
-    cols = t.shape[-1]
-    rows = t.numel() // cols if cols else 0
-    if t.is_contiguous():
-        return rows, cols, cols
-    if t.dim() != 2 or (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < cols):
-        raise ValueError(f"{name}: expected dense rows, got strides {tuple(t.stride())}")
-    return rows, cols, t.stride(0) if rows > 1 else cols
-
-
-def _act8_dtype(t, name):
-    import torch
-    if t.dtype == torch.bfloat16:
-        return VMOBA_BF16
-    if t.dtype == torch.float32:
-        return VMOBA_F32
-    raise ValueError(f"{name}: expected dtype bfloat16 or float32, got {t.dtype}")
-
-
-def act8_pack(x, ckpt, stream=None):
-    """Store an activation in 8 bits: x (bf16 or fp32, [rows][cols] with rows
-    any stride apart, or contiguous with more axes) into ``ckpt``."""
-    c = _Call("vmoba_act8_pack")
-    rows, cols, ld = _act8_rows(x, "x")
-    dt, at = _act8_dtype(x, "x"), c.addr(x, x.shape, x.dtype, "x", strided=True)
-    codes, scales = c.ckpt(ckpt, tuple(x.shape), ckpt.group, "ckpt")
-    c.run(stream, dt, at, rows, cols, ld, ckpt.group, codes, scales)
-
-
-def act8_unpack(ckpt, out, stream=None):
-    """Read an 8-bit checkpoint back into ``out`` (bf16 or fp32, laid out as
-    act8_pack's x)."""
-    c = _Call("vmoba_act8_unpack")
-    rows, cols, ld = _act8_rows(out, "out")
-    dt, at = _act8_dtype(out, "out"), c.addr(out, out.shape, out.dtype, "out", strided=True)
-    codes, scales = c.ckpt(ckpt, tuple(out.shape), ckpt.group, "ckpt")
-    c.run(stream, dt, codes, scales, rows, cols, ckpt.group, at, ld)
 
 
 def debug_set_wait(wait_cycles: int = 0, skip_forward_loads: bool = False) -> None:

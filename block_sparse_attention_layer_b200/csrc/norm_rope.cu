@@ -307,9 +307,8 @@ k_norm_rope(const __grid_constant__ Walk w, const __grid_constant__ NormRopeArgs
 class Capacity {
  public:
   template <typename K>
-  int ctas(K kernel, int cluster, int smem, int num_sms) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return num_sms;
+  int ctas(K kernel, int dev, int cluster, int smem, int num_sms) {
+    if (dev < 0 || dev >= kDevices) return num_sms;
     std::atomic<int>& known = known_[dev][cluster];
     int n = known.load(std::memory_order_relaxed);
     if (n) return n;
@@ -344,7 +343,9 @@ cudaError_t launch_t(const Prob& P, const NormRopeArgs& a, const NormRopeOut& o,
   const auto kernel = k_norm_rope<E, D, From8, To8, TwoHeads>;
   static SmemOptIn opt_in;
   static Capacity capacity;
-  cudaError_t e = opt_in.set(kernel, M::kBytes);
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = opt_in.set(kernel, M::kBytes, dev);
   if (e != cudaSuccess) return e;
   const int units = TwoHeads ? P.n_h / 2 : P.n_h;
   Walk w{};
@@ -364,7 +365,7 @@ cudaError_t launch_t(const Prob& P, const NormRopeArgs& a, const NormRopeOut& o,
       const int step = kWarps / up * R;
       for (int c = 1; c <= 8 && c <= P.L; ++c) {
         const long long ctas = (long long)P.Nb * c * (units / up);
-        const int slots = capacity.ctas(kernel, c, M::kBytes, num_sms);
+        const int slots = capacity.ctas(kernel, dev, c, M::kBytes, num_sms);
         const long long cost =
             ((ctas + slots - 1) / slots) * (((P.L + c - 1) / c + step - 1) / step + 2);
         if (best < 0 || cost < best) {

@@ -291,7 +291,10 @@ cudaError_t launch_t(const Prob& P, const NormRopeArgs& a, const void* dq, const
   const auto kernel = k_norm_rope_bwd<E, D, From8, TwoHeads>;
   constexpr int smem = Smem<E, D, From8, TwoHeads>::kBytes;
   static SmemOptIn opt_in;
-  if (const cudaError_t e = opt_in.set(kernel, smem); e != cudaSuccess) return e;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = opt_in.set(kernel, smem, dev);
+  if (e != cudaSuccess) return e;
   {
     VMOBA_TRACE("k_norm_rope_bwd", st);
     kernel<<<ctas, kThreads, smem, st>>>(
@@ -299,7 +302,7 @@ cudaError_t launch_t(const Prob& P, const NormRopeArgs& a, const void* dq, const
         static_cast<E*>(out[0]), static_cast<E*>(out[1]), static_cast<E*>(out[2]), part);
   }
   count_launches(1);
-  cudaError_t e = cudaGetLastError();
+  e = cudaGetLastError();
   if (e != cudaSuccess || !dweight) return e;
   {
     VMOBA_TRACE("k_norm_dweight", st);

@@ -590,11 +590,9 @@ __device__ __forceinline__ Vals load_weights(const float* g, int l) {
 class SmemOptIn {
  public:
   template <typename K>
-  cudaError_t set(K kernel, int bytes) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess || (dev < 64 && (done_.load() >> dev & 1))) return e;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  cudaError_t set(K kernel, int bytes, int dev) {
+    if (dev < 64 && (done_.load(std::memory_order_relaxed) >> dev & 1)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e == cudaSuccess && dev < 64) done_.fetch_or(1ull << dev);
     return e;
   }

@@ -7,7 +7,7 @@ import numpy as np
 import pytest
 
 import block_sparse_attention_layer_b200 as V
-from block_sparse_attention_layer_b200 import _lib
+from block_sparse_attention_layer_b200 import _lib, norm_rope
 
 from . import norm_rope_ref as R
 
@@ -116,21 +116,40 @@ def test_workspace_sizes():
     assert V.qk_norm_rope_bwd_workspace_size(_shape(bt=3)) == 0
 
 
+class _Fake:
+    """A stand-in with a CUDA tensor's attributes: what the layout checks read."""
+
+    def __init__(self, t, device="cuda:0"):
+        self.t, self.device = t, torch.device(device)
+        self.shape, self.dtype, self.is_cuda = t.shape, t.dtype, True
+        self.get_device = lambda: self.device.index
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+
 def test_binding_refuses_before_the_call():
     sh = _shape()
     s, h, d = sh.s, 2, 64
     bf = torch.bfloat16
-    t = torch.zeros((s, h, d), dtype=bf)
-    qkv = torch.zeros((s, 3, h, d), dtype=bf)
+    host = torch.zeros((s, h, d), dtype=bf)
+    t, qkv = _Fake(host), torch.zeros((s, 3, h, d), dtype=bf)
     nr = V.NormRope()
-    with pytest.raises(ValueError, match="CUDA"):
-        V.qk_norm_rope(sh, nr, qkv, t, t, t)
-    with pytest.raises(ValueError, match="shape"):
-        V.qk_norm_rope(sh, nr, qkv[1:], t, t, t)
-    with pytest.raises(ValueError, match="dtype"):
-        V.qk_norm_rope(sh, nr, qkv.float(), t, t, t)
-    with pytest.raises(ValueError, match="one tensor or three"):
-        V.qk_norm_rope(sh, nr, (t, t), t, t, t)
+    for match, call in (
+            ("q: expected a CUDA", lambda: V.qk_norm_rope(sh, nr, qkv, host, t, t)),
+            ("qkv: expected a CUDA", lambda: V.qk_norm_rope(sh, nr, qkv, t, t, t)),
+            ("v: expected a CUDA", lambda: V.qk_norm_rope(sh, nr, _Fake(qkv), t, t, host)),
+            ("k: expected a tensor on cuda:0",
+             lambda: V.qk_norm_rope(sh, nr, _Fake(qkv), t, _Fake(host, "cuda:1"), t)),
+            ("qkv: expected shape", lambda: V.qk_norm_rope(sh, nr, _Fake(qkv[1:]), t, t, t)),
+            ("qkv: expected dtype", lambda: V.qk_norm_rope(sh, nr, _Fake(qkv.float()), t, t, t)),
+            ("one tensor or three", lambda: V.qk_norm_rope(sh, nr, (t, t), t, t, t)),
+            ("k: expected a contiguous",
+             lambda: V.qk_norm_rope(sh, nr, _Fake(qkv), t, _Fake(qkv[:, 0]), t)),
+            ("blocks: expected a tensor",
+             lambda: V.qk_norm_rope_partition(sh, nr, _Fake(qkv), t, t, t, None))):
+        with pytest.raises(ValueError, match=match):
+            call()
     with pytest.raises(ValueError, match="checkpoint"):
         c = V.Act8.empty((s, 3, h, d), d, "cpu")
         V.qk_norm_rope(sh, nr, c, t, t, t, ckpt=c)
@@ -144,18 +163,10 @@ def test_binding_refuses_before_the_call():
         V.act8_pack(torch.zeros(4), V.Act8.empty((4,), 64, "cpu"))
     with pytest.raises(ValueError, match="dense rows"):
         V.act8_pack(torch.zeros((4, 8)).t(), V.Act8.empty((8, 4), 64, "cpu"))
-
-
-class _Fake:
-    """A stand-in with a CUDA tensor's attributes: what the layout checks read."""
-
-    def __init__(self, t, device="cuda:0"):
-        self.t, self.device = t, torch.device(device)
-        self.shape, self.dtype, self.is_cuda = t.shape, t.dtype, True
-        self.get_device = lambda: self.device.index
-
-    def __getattr__(self, name):
-        return getattr(self.t, name)
+    with pytest.raises(ValueError, match="dense rows"):
+        V.act8_unpack(V.Act8.empty((4, 8), 64, "cpu"), torch.zeros((1, 8)).expand(4, 8))
+    with pytest.raises(ValueError, match="CUDA"):
+        V.act8_pack(torch.zeros((4, 8)), V.Act8.empty((4, 8), 64, "cpu"))
 
 
 def test_raw_rows_layouts():
@@ -164,17 +175,17 @@ def test_raw_rows_layouts():
     bf = torch.bfloat16
 
     def raw(x):
-        return _lib._Call("x").raw(sh, x, bf, "qkv")
+        return norm_rope._raw(sh, x, 0, "qkv")
 
     base = torch.zeros((s, 3 * h * d + 64), dtype=bf)
     x = base.as_strided((s, 3, h, d), (base.stride(0), h * d, d, 1))
-    at, ld = raw(_Fake(x))
+    *at, ld = raw(_Fake(x))
     assert ld == 3 * h * d + 64 and [a - at[0] for a in at] == [0, 2 * h * d, 4 * h * d]
     three = [torch.zeros((s, h, d), dtype=bf) for _ in range(3)]
-    at, ld = raw([_Fake(t) for t in three])
+    *at, ld = raw([_Fake(t) for t in three])
     assert ld == h * d and at == [t.data_ptr() for t in three]
     packed = torch.zeros((s, 3, h, d), dtype=bf)
-    at, ld = raw([_Fake(packed[:, i]) for i in range(3)])
+    *at, ld = raw([_Fake(packed[:, i]) for i in range(3)])
     assert ld == 3 * h * d
     with pytest.raises(ValueError, match="one token stride"):
         raw([_Fake(three[0]), _Fake(three[1]), _Fake(packed[:, 2])])
@@ -192,7 +203,7 @@ def test_raw_rows_layouts():
     (dict(q_weight=torch.zeros(32)), "q_weight"), (dict(k_weight=torch.zeros(64)), "CUDA")])
 def test_norm_arguments_refused(kw, match):
     with pytest.raises(ValueError, match=match):
-        _lib._Call("x").norm(_shape(), V.NormRope(**kw))
+        norm_rope._norm(_shape(), V.NormRope(**kw), 0)
 
 
 def test_rope_dims():
