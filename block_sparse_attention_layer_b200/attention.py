@@ -14,10 +14,21 @@ from __future__ import annotations
 import math
 
 import torch
+from torch.autograd.function import once_differentiable
 
-from . import _lib
+from . import _lib, norm_rope
 from ._lib import LayerShape
 from .layer import VMoBALayer
+from .norm_rope import Act8, NormRope
+
+
+def _all_pairs(layer: VMoBALayer) -> torch.Tensor:
+    """The selection bitmap of dense attention over the layer's blocks."""
+    bits = torch.full_like(layer.sel, -1)
+    rem = layer.n_blocks % 32
+    if rem:
+        bits[..., -1] = (1 << rem) - 1
+    return bits
 
 
 class VMoBAFunction(torch.autograd.Function):
@@ -40,13 +51,8 @@ class VMoBAFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, layer: VMoBALayer, tau: float, full: bool, scale: float):
         if full:
-            nb = layer.n_blocks
-            bits = torch.full_like(layer.sel, -1)
-            rem = nb % 32
-            if rem:
-                bits[..., -1] = (1 << rem) - 1
             layer.partition_only(k, v)
-            layer.use_selection(bits)
+            layer.use_selection(_all_pairs(layer))
         else:
             layer.select(q, k, v, tau, scale)
         out, _ = layer.forward(q, scale)
@@ -69,6 +75,90 @@ class VMoBAFunction(torch.autograd.Function):
         return dq.clone(), dk.clone(), dv.clone(), None, None, None, None
 
 
+class VMoBANormRopeFunction(torch.autograd.Function):
+    """O = VMoBA(rot(norm(q)), rot(norm(k)), v) of the projection's raw rows
+    qkv [s][3][n_heads][head_dim]; the norm weights are fp32 [head_dim] or
+    None (ones), table and dims the rotation's (norm_rope.rope_table).
+
+    Saved for the backward are the raw rows, or with ``checkpoint8`` their
+    8-bit checkpoint (written by the forward's own pass), and the selection.
+    The other state stays in the layer's buffers; if another forward ran on
+    the layer in between, the backward rebuilds it from what was saved: from
+    the raw rows bit for bit, from a checkpoint as the attention of the values
+    it holds.  The gradients of the raw rows and norm weights are taken at the
+    saved values in either case.
+    """
+
+    @staticmethod
+    def forward(ctx, qkv, q_weight, k_weight, layer: VMoBALayer, table, dims, eps: float,
+                tau: float, full: bool, scale: float, checkpoint8: bool):
+        norm = NormRope(q_weight, k_weight, eps, table, dims)
+        ckpt = Act8.empty(qkv.shape, layer.shape.head_dim, qkv.device) if checkpoint8 else None
+        layer.prologue(qkv, norm, ckpt)
+        if full:
+            layer.use_selection(_all_pairs(layer))
+        else:
+            layer.select_pooled(layer.q, tau, scale)
+        out, _ = layer.forward(layer.q, scale)
+        ctx.layer, ctx.scale, ctx.dims, ctx.eps = layer, scale, dims, eps
+        ctx.generation = layer.generation
+        ctx.has = q_weight is not None, k_weight is not None, table is not None, checkpoint8
+        given = [t for t in (q_weight, k_weight, table) if t is not None]
+        ctx.save_for_backward(layer.sel.clone(), *given,
+                              *((ckpt.codes, ckpt.scales) if checkpoint8 else (qkv,)))
+        return out.clone()
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dout):
+        layer, saved = ctx.layer, list(ctx.saved_tensors)
+        sel = saved.pop(0)
+        q_weight, k_weight, table = (saved.pop(0) if has else None for has in ctx.has[:3])
+        norm = NormRope(q_weight, k_weight, ctx.eps, table, ctx.dims)
+        raw = Act8(*saved, layer.shape.head_dim) if ctx.has[3] else saved[0]
+        if layer.generation != ctx.generation:
+            # another forward replaced this call's state: rebuild it
+            layer.prologue(raw, norm)
+            layer.use_selection(sel)
+            layer.forward(layer.q, ctx.scale)
+            ctx.generation = layer.generation
+        s, h, d = layer.shape.s, layer.shape.n_heads, layer.shape.head_dim
+        dqkv = torch.empty((s, 3, h, d), dtype=layer.dtype, device=dout.device)
+        need_q, need_k = ctx.needs_input_grad[1:3]
+        dweight = torch.empty((2, d), dtype=torch.float32, device=dout.device) \
+            if need_q or need_k else None
+        layer.backward_raw(raw, norm, dout.contiguous(), dqkv, dweight, ctx.scale)
+        return (dqkv, dweight[0] if need_q else None, dweight[1] if need_k else None) + (None,) * 8
+
+
+class Linear8Function(torch.autograd.Function):
+    """y = x W^T + b, x [rows][cols] kept for the weight's gradient as an 8-bit
+    checkpoint: dx = dy W, dW = dy^T x8, db = sum dy."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias):
+        ckpt = Act8.empty(x.shape, 128 if x.shape[1] % 128 == 0 else 64, x.device)
+        norm_rope.act8_pack(x, ckpt)
+        ctx.group, ctx.x_dtype = ckpt.group, x.dtype
+        ctx.save_for_backward(ckpt.codes, ckpt.scales, weight)
+        return torch.nn.functional.linear(x, weight, bias)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        codes, scales, weight = ctx.saved_tensors
+        dx = dw = db = None
+        if ctx.needs_input_grad[0]:
+            dx = dy @ weight
+        if ctx.needs_input_grad[1]:
+            x = torch.empty(codes.shape, dtype=ctx.x_dtype, device=codes.device)
+            norm_rope.act8_unpack(Act8(codes, scales, ctx.group), x)
+            dw = dy.t() @ x
+        if ctx.needs_input_grad[2]:
+            db = dy.sum(0)
+        return dx, dw, db
+
+
 class VMoBASelfAttention(torch.nn.Module):
     """Self-attention of one DiT layer over a (T, H, W) video latent with
     VMoBA in place of full attention.
@@ -77,11 +167,25 @@ class VMoBASelfAttention(torch.nn.Module):
     (bt, bh, bw) box of each partition mode (mode = layer_idx mod 3);
     ``full_attention=True`` in ``forward`` keeps every pair (the early
     denoising steps of the training strategy).
+
+    ``qk_norm`` normalises each head's query and key (RMS norm with fp32
+    weights ``q_norm``, ``k_norm`` of head_dim); ``rope`` then rotates them by
+    the token's position, with that many of a head's dimensions for t, y and x
+    (``True``: the usual split, norm_rope.rope_dims), frequencies
+    ``rope_base`` ** (-2i / dim), positions counted from ``rope_origin``.
+    ``checkpoint8`` keeps what the backward needs of the activations in 8 bits:
+    the projections' inputs and the raw q, k, v (5 bytes and 5 scales of a
+    group for each token and channel in place of 10 in bf16).  Rotation and
+    checkpoints are part of the norm's pass, so both need ``qk_norm``.
     """
 
     def __init__(self, dim: int, n_heads: int, T: int, H: int, W: int, layer_idx: int,
-                 boxes, tau: float = 0.25, dtype=torch.bfloat16, device="cuda"):
+                 boxes, tau: float = 0.25, dtype=torch.bfloat16, device="cuda", *,
+                 qk_norm: bool = False, norm_eps: float = 1e-6, rope=None,
+                 rope_base: float = 10000.0, rope_origin=(0, 0, 0), checkpoint8: bool = False):
         super().__init__()
+        if not qk_norm and (rope or checkpoint8):
+            raise ValueError("rope and checkpoint8 need qk_norm")
         if dim % n_heads:
             raise ValueError("dim must be a multiple of n_heads")
         self.n_heads, self.head_dim = n_heads, dim // n_heads
@@ -94,9 +198,29 @@ class VMoBASelfAttention(torch.nn.Module):
         self.shape = LayerShape(T, H, W, n_heads, self.head_dim, self.mode, bt, bh, bw, dt)
         self.layer = VMoBALayer(self.shape, device=device)
         self.scale = 1.0 / math.sqrt(self.head_dim)
+        self.norm_eps, self.checkpoint8 = float(norm_eps), bool(checkpoint8)
+        self.rope_dims = (0, 0, 0)
+        self.q_norm = self.k_norm = None
+        if qk_norm:
+            self.q_norm, self.k_norm = (
+                torch.nn.Parameter(torch.ones(self.head_dim, dtype=torch.float32, device=device))
+                for _ in range(2))
+        if rope:
+            self.rope_dims = norm_rope.rope_dims(self.head_dim) if rope is True else tuple(rope)
+            self.register_buffer("rope_table", norm_rope.rope_table(
+                self.shape, self.rope_dims, rope_base, rope_origin, device), persistent=False)
 
     def forward(self, x: torch.Tensor, full_attention: bool = False) -> torch.Tensor:
         s = x.shape[0]
+        if self.q_norm is not None:
+            keep8 = self.checkpoint8 and torch.is_grad_enabled()
+            linear = Linear8Function.apply if keep8 else torch.nn.functional.linear
+            qkv = linear(x, self.qkv.weight, self.qkv.bias)
+            o = VMoBANormRopeFunction.apply(
+                qkv.view(s, 3, self.n_heads, self.head_dim), self.q_norm, self.k_norm, self.layer,
+                getattr(self, "rope_table", None), self.rope_dims, self.norm_eps, self.tau,
+                bool(full_attention), self.scale, keep8)
+            return linear(o.view(s, -1), self.proj.weight, self.proj.bias)
         qkv = self.qkv(x).view(s, 3, self.n_heads, self.head_dim)
         q, k, v = (qkv[:, i].contiguous() for i in range(3))
         o = VMoBAFunction.apply(q, k, v, self.layer, self.tau, bool(full_attention), self.scale)

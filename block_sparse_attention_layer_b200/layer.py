@@ -7,9 +7,11 @@ current CUDA stream.  All arithmetic runs in libvmoba's kernels.
 """
 from __future__ import annotations
 
+import functools
+
 import torch
 
-from . import _lib
+from . import _lib, norm_rope
 from ._lib import LayerShape
 
 
@@ -46,6 +48,43 @@ class VMoBALayer:
         # forwards run so far: lets a caller tell whether the forward state in
         # the buffers (LSE, fp32 output copy, pair lists) is still its own
         self.generation = 0
+        self._device = dev
+
+    # buffers of the calls that start from the projection's raw rows, made
+    # when they are first used
+
+    @functools.cached_property
+    def q(self):
+        """The normalised and rotated queries of the last ``prologue``."""
+        sh = self.shape
+        return torch.empty((sh.s, sh.n_heads, sh.head_dim), dtype=self.dtype, device=self._device)
+
+    @functools.cached_property
+    def ws_norm(self):
+        return torch.empty((norm_rope.qk_norm_rope_bwd_workspace_size(self.shape),),
+                           dtype=torch.uint8, device=self._device)
+
+    def prologue(self, qkv, norm, ckpt=None):
+        """Raw rows of the projection (or their Act8 checkpoint) -> self.q,
+        self.k_perm, self.v_perm and self.blocks: norm, rotation, partition
+        and pooling in one pass (norm_rope.qk_norm_rope_partition); ckpt: an
+        Act8 to store the raw rows in."""
+        norm_rope.qk_norm_rope_partition(self.shape, norm, qkv, self.q, self.k_perm, self.v_perm,
+                                         self.blocks, ckpt=ckpt)
+
+    def select_pooled(self, q, tau, scale=0.0):
+        """Selection and plan from the block means already in self.blocks."""
+        sh = self.shape
+        _lib.score_select(sh, q, self.blocks, tau, scale, self.sel, self.stats, self.ws)
+        _lib.build_plan(sh, self.sel, self.ws)
+
+    def backward_raw(self, qkv, norm, dout, dqkv, dweight=None, scale=0.0):
+        """Attention backward of the last prologue + forward, then through
+        rotation and norm: gradients of the raw rows into dqkv and of the two
+        norm weights into dweight.  qkv: the raw rows or their checkpoint."""
+        self.backward(self.q, dout, scale)
+        norm_rope.qk_norm_rope_bwd(self.shape, norm, qkv, self.dq, self.dk, self.dv, dqkv, dweight,
+                                   self.ws_norm if dweight is not None else None)
 
     def select(self, q, k, v, tau, scale=0.0):
         sh = self.shape
