@@ -41,7 +41,7 @@ struct Walk {
   int chunk, chunks;               // rows of a chunk, chunks of a block
   int up;                          // units of heads of a CTA
   int still;                       // whether some pairs do not turn
-  uint32_t ld, kv_tok;             // bytes between tokens of the raw rows; positions of k and v
+  uint32_t ld, q_tok, kv_tok;      // bytes between tokens of the raw rows and q; positions of k, v
   long long kv_head;               // elements between heads of k and v
 };
 
@@ -49,13 +49,19 @@ struct Walk {
 template <typename E, int D, bool From8, bool TwoHeads>
 struct Feed {
   static constexpr int kSlot = Slot<E, D>::kBytes, kBytes = 6 * kSlot;
-  __device__ __forceinline__ static void ask(char* s, const Walk& w, const NormRopeArgs& a, int n,
-                                             int h, int u, int sub, int l) {
+  const char* in[3];                 // the lane's first 16 bytes of head h0, token 0
+  __device__ __forceinline__ Feed(const Walk& w, const NormRopeArgs& a, int h0, int l) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      in[i] = pinned(static_cast<const char*>(a.in[i]) + h0 * D * (int)sizeof(E) + l * 16);
+  }
+  __device__ __forceinline__ void ask(char* s, const Walk& w, int n, int u, int sub,
+                                      int l) const {
 #pragma unroll
     for (int i = 0; i < 3; ++i)
       Slot<E, D>::ask(s + (3 * u + i) * kSlot,
-                      at_bytes(static_cast<const E*>(a.in[i]) + h * D, n, w.ld),
-                      sub * (D / 8) + l, l);
+                      at_bytes(in[i], n, w.ld) + (TwoHeads ? u * D * (int)sizeof(E) : 0),
+                      sub * (D / 8) + l);
   }
   __device__ __forceinline__ static Raw<E> raw(const char* s, int i, int u, int sub, int l) {
     return Slot<E, D>::get(s + (3 * u + i) * kSlot, sub * (D / 8) + l);
@@ -76,9 +82,16 @@ template <typename E, int D, bool TwoHeads>
 struct Feed<E, D, true, TwoHeads> {
   using C = CodeRows<E, D, 3, TwoHeads>;
   static constexpr int kBytes = C::kBytes;
-  __device__ __forceinline__ static void ask(char* s, const Walk& w, const NormRopeArgs& a, int n,
-                                             int h, int u, int sub, int l) {
-    C::ask(s, a.codes, a.scales, n, h, w.n_h, u, sub, l);
+  const char* codes[3];
+  const float* scale;
+  __device__ __forceinline__ Feed(const Walk& w, const NormRopeArgs& a, int h0, int l) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) codes[i] = pinned(C::codes_at(a.codes, i, h0, w.n_h, l));
+    scale = pinned(C::scale_at(a.scales, h0, w.n_h, l));
+  }
+  __device__ __forceinline__ void ask(char* s, const Walk& w, int n, int u, int sub,
+                                      int l) const {
+    C::ask(s, codes, scale, n, w.n_h, u, sub, l);
   }
   __device__ __forceinline__ static void load(const char* s, float eps, int sub, int l,
                                               Vals (&x)[4]) {
@@ -171,6 +184,7 @@ k_norm_rope(const __grid_constant__ Walk w, const __grid_constant__ NormRopeArgs
     const int t = t0 + bt, y = y0 + by, x = x0 + rest - by * w.bw;
     return Spot{{t * a.ht, y_rows + y * a.hh, x_rows + x * a.hw}, (t * w.H + y) * w.W + x};
   };
+  const F feed(w, a, h0, l);
   auto ask = [&](int r0, int stage) {
     if (r0 < last) {
       int n = 0;
@@ -181,13 +195,25 @@ k_norm_rope(const __grid_constant__ Walk w, const __grid_constant__ NormRopeArgs
           n = spot.n;
           if (l == 0) spots[stage * 8 + u * 4 + sub] = spot;
         }
-        F::ask(ring + stage * F::kBytes, w, a, n, h0 + (TwoHeads ? u : 0), u, sub, l);
+        feed.ask(ring + stage * F::kBytes, w, n, u, sub, l);
       }
     }
     fetch_commit();
   };
 #pragma unroll
   for (int i = 0; i < S - 1; ++i) ask(r_begin + i * stride, i);
+  // the lane's first bytes of head h0, token or position 0
+  char* const to_q = pinned(static_cast<char*>(o.q) + h0 * D * (int)sizeof(E) + l * 16);
+  char* const to_k =
+      pinned(static_cast<char*>(o.k) + h0 * w.kv_head * (int)sizeof(E) + l * 16);
+  char* const to_v =
+      pinned(static_cast<char*>(o.v) + h0 * w.kv_head * (int)sizeof(E) + l * 16);
+  [[maybe_unused]] char* to_codes = nullptr;
+  [[maybe_unused]] float* to_scales = nullptr;
+  if constexpr (To8) {
+    to_codes = pinned(reinterpret_cast<char*>(o.codes) + h0 * D + l * (sizeof(E) == 2 ? 8 : 4));
+    to_scales = pinned(o.scales + h0);
+  }
   int rows = 0, stage = 0;
   for (int r0 = r_begin; r0 < last; r0 += stride) {
     __syncwarp();                    // the spots of the stage that is refilled have been read
@@ -222,18 +248,19 @@ k_norm_rope(const __grid_constant__ Walk w, const __grid_constant__ NormRopeArgs
         group_max<G>(raw[0], raw[1], m[0], m[1]);
 #pragma unroll
         for (int u = 0; u < 2; ++u) c[u] = encode8<E>(unpack(raw[u]), m[u], sc[u]);
-        const uint32_t row[2] = {(uint32_t)((n[0] * 3 + i) * w.n_h + h0),
-                                 (uint32_t)((n[1] * 3 + i) * w.n_h + h0 + (TwoHeads ? 1 : 0))};
+        // row (n, i) of the checkpoint: n_h heads of D codes
+        const int row[2] = {(n[0] * 3 + i) * w.n_h, (n[1] * 3 + i) * w.n_h};
 #pragma unroll
         for (int u = 0; u < 2; ++u)
-          if (mine[u]) store_codes<E, D>(at_bytes(o.codes, row[u], D), l, c[u]);
+          if (mine[u])
+            store_codes<E, D>(at_bytes(to_codes, row[u], D) + (TwoHeads ? u * D : 0), c[u]);
         if (l == 0) {
           if constexpr (TwoHeads) {      // an even row: two scales in one access
             if (mine[0])
-              *reinterpret_cast<float2*>(o.scales + row[0]) = make_float2(sc[0], sc[1]);
+              *reinterpret_cast<float2*>(to_scales + row[0]) = make_float2(sc[0], sc[1]);
           } else {
-            if (mine[0]) o.scales[row[0]] = sc[0];
-            if (mine[1]) o.scales[row[1]] = sc[1];
+            if (mine[0]) to_scales[row[0]] = sc[0];
+            if (mine[1]) to_scales[row[1]] = sc[1];
           }
         }
       }
@@ -251,15 +278,15 @@ k_norm_rope(const __grid_constant__ Walk w, const __grid_constant__ NormRopeArgs
       turn(q, cs[TwoHeads ? 0 : u]);
       turn(k, cs[TwoHeads ? 0 : u]);
       if (mine[u]) {
-        const int h = h0 + (TwoHeads ? u : 0);
         Raw<E> s;
         pack(q, s);
-        store_raw<D>(at_bytes(static_cast<E*>(o.q) + h * D, n[u], w.n_h * D * sizeof(E)), l, s);
+        Slot<E, D>::put(at_bytes(to_q, n[u], w.q_tok) + (TwoHeads ? u * D * (int)sizeof(E) : 0),
+                        s);
         pack(k, s);
         const int p = j * w.L + r[u];
-        store_raw<D>(at_bytes(static_cast<E*>(o.k) + h * w.kv_head, p, w.kv_tok), l, s);
-        store_raw<D>(at_bytes(static_cast<E*>(o.v) + h * w.kv_head, p, w.kv_tok), l,
-                     F::value(in, u, sub, l));
+        const long long head = TwoHeads && u ? w.kv_head * (int)sizeof(E) : 0;
+        Slot<E, D>::put(at_bytes(to_k, p, w.kv_tok) + head, s);
+        Slot<E, D>::put(at_bytes(to_v, p, w.kv_tok) + head, F::value(in, u, sub, l));
         Vals& to = acc[TwoHeads ? u : 0];
 #pragma unroll
         for (int i = 0; i < 4; ++i) to.p[i] = __fadd2_rn(to.p[i], k.p[i]);
@@ -353,6 +380,7 @@ cudaError_t launch_t(const Prob& P, const NormRopeArgs& a, const NormRopeOut& o,
   w.bt = P.bt; w.bh = P.bh; w.bw = P.bw;
   w.nbh = P.nbh; w.nbw = P.nbw; w.Nb = P.Nb; w.L = P.L;
   w.ld = (uint32_t)(a.ld * sizeof(E));
+  w.q_tok = P.n_h * D * sizeof(E);
   w.still = 2 * (a.ht + a.hh + a.hw) < D;
   if (o.blocks) {
     w.kv_tok = D * sizeof(E);

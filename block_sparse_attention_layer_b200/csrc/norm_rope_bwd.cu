@@ -124,6 +124,21 @@ k_norm_rope_bwd(const __grid_constant__ Walk w, const __grid_constant__ NormRope
   enter(cur);
   skip_empty(cur);
   At ahead = cur;
+  // the lane's first bytes of head 0, token 0
+  const char* in_dq = reinterpret_cast<const char*>(dq) + l * 16;
+  const char* in_dk = reinterpret_cast<const char*>(dk) + l * 16;
+  const char* in_dv = reinterpret_cast<const char*>(dv) + l * 16;
+  const char* in_raw[2];
+  [[maybe_unused]] const float* in_scale = nullptr;
+  if constexpr (From8) {
+    for (int i = 0; i < 2; ++i) in_raw[i] = F::C::codes_at(a.codes, i, 0, w.n_h, l);
+    in_scale = F::C::scale_at(a.scales, 0, w.n_h, l);
+  } else {
+    for (int i = 0; i < 2; ++i) in_raw[i] = static_cast<const char*>(a.in[i]) + l * 16;
+  }
+  char* const to_q = reinterpret_cast<char*>(oq) + l * 16;
+  char* const to_k = reinterpret_cast<char*>(ok) + l * 16;
+  char* const to_v = reinterpret_cast<char*>(ov) + l * 16;
   auto ask = [&](int stage) {
     if (ahead.item < w.n_items) {
       int n = 0;
@@ -137,19 +152,20 @@ k_norm_rope_bwd(const __grid_constant__ Walk w, const __grid_constant__ NormRope
                 Spot{{t * a.ht, y_rows + y * a.hh, x_rows + (yx - y * w.W) * a.hw}, n};
           }
         }
-        const int h = ahead.h0 + (TwoHeads ? u : 0);
         char* to = ring + stage * F::kBytes;
-        Slot<E, D>::ask(to + 3 * u * F::kSlot, at_bytes(dq + h * D, n, row3), lane, l);
-        Slot<E, D>::ask(to + (3 * u + 1) * F::kSlot, at_bytes(dk + h * D, n, row3), lane, l);
-        Slot<E, D>::ask(to + (3 * u + 2) * F::kSlot, at_bytes(dv + h * D, n, row3), lane, l);
+        const long long more = (ahead.h0 + (TwoHeads ? u : 0)) * (long long)(D * sizeof(E));
+        Slot<E, D>::ask(to + 3 * u * F::kSlot, at_bytes(in_dq, n, row3) + more, lane);
+        Slot<E, D>::ask(to + (3 * u + 1) * F::kSlot, at_bytes(in_dk, n, row3) + more, lane);
+        Slot<E, D>::ask(to + (3 * u + 2) * F::kSlot, at_bytes(in_dv, n, row3) + more, lane);
         to += F::kRaw;
         if constexpr (From8) {
-          F::C::ask(to, a.codes, a.scales, n, h, w.n_h, u, sub, l);
+          const char* const codes[2] = {in_raw[0] + (long long)ahead.h0 * D,
+                                        in_raw[1] + (long long)ahead.h0 * D};
+          F::C::ask(to, codes, in_scale + ahead.h0, n, w.n_h, u, sub, l);
         } else {
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            Slot<E, D>::ask(to + (2 * u + i) * F::kSlot,
-                            at_bytes(static_cast<const E*>(a.in[i]) + h * D, n, w.ld), lane, l);
+            Slot<E, D>::ask(to + (2 * u + i) * F::kSlot, at_bytes(in_raw[i], n, w.ld) + more, lane);
         }
       }
       ahead.n0 += kStride;
@@ -191,8 +207,9 @@ k_norm_rope_bwd(const __grid_constant__ Walk w, const __grid_constant__ NormRope
 #pragma unroll
       for (int u = 0; u < 2; ++u)
         if (mine[u])
-          store_raw<D>(at_bytes(ov + (h0 + (TwoHeads ? u : 0)) * D, n[u], w.ld_out), l,
-                       F::grad(in, 2, u, lane));
+          Slot<E, D>::put(at_bytes(to_v, n[u], w.ld_out) +
+                              (h0 + (TwoHeads ? u : 0)) * (long long)(D * sizeof(E)),
+                          F::grad(in, 2, u, lane));
       Vals x[4];
       float r[4], dot[4];
       F::load(in, a.eps, sub, l, x, r);          // xh = x r
@@ -218,8 +235,9 @@ k_norm_rope_bwd(const __grid_constant__ Walk w, const __grid_constant__ NormRope
         if (mine[k / 2]) {
           Raw<E> s;
           pack(g[k], s);
-          const int h = h0 + (TwoHeads ? k / 2 : 0);
-          store_raw<D>(at_bytes((k & 1 ? ok : oq) + h * D, n[k / 2], w.ld_out), l, s);
+          Slot<E, D>::put(at_bytes(k & 1 ? to_k : to_q, n[k / 2], w.ld_out) +
+                              (h0 + (TwoHeads ? k / 2 : 0)) * (long long)(D * sizeof(E)),
+                          s);
         }
       }
     }

@@ -68,16 +68,6 @@ __device__ __forceinline__ float4 as_float4(const uint4& v) {
                      __uint_as_float(v.w));
 }
 
-template <int D>
-__device__ __forceinline__ Raw<__nv_bfloat16> load_row(const __nv_bfloat16* row, int l) {
-  return {load16(reinterpret_cast<const uint4*>(row) + l)};
-}
-template <int D>
-__device__ __forceinline__ Raw<float> load_row(const float* row, int l) {
-  const float4* p = reinterpret_cast<const float4*>(row);
-  return {as_float4(load16(p + l)), as_float4(load16(p + D / 8 + l))};
-}
-
 // Asynchronous copies of a lane's own values into its own place in shared
 // memory: only the lane that asked for them reads them, so its own wait is the
 // only one needed, and loads stay in flight without holding registers.
@@ -96,20 +86,27 @@ __device__ __forceinline__ void fetch_wait() {
   asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory");
 }
 
+// A lane's pointer into one tensor, held in registers through a loop (the
+// compiler otherwise forms it anew at every use), and `n` strides from it.
+template <typename T>
+__device__ __forceinline__ T* pinned(T* p) {
+  asm volatile("" : "+l"(p));
+  return p;
+}
 template <typename T>
 __device__ __forceinline__ T* at_bytes(T* p, int n, uint32_t stride) {
   return reinterpret_cast<T*>(
       reinterpret_cast<uintptr_t>(p) + (unsigned long long)(uint32_t)n * stride);
 }
 
-// A warp's place for one access of its R rows, in the order of the lanes.
+// A warp's place for one access of its R rows, in the order of the lanes;
+// `from` is where the lane's first 16 bytes lie.
 template <typename E, int D>
 struct Slot {
   static constexpr int kBytes = 32 * sizeof(Raw<E>);
-  __device__ __forceinline__ static void ask(char* s, const E* row, int lane, int l) {
-    fetch<16>(s + lane * 16, reinterpret_cast<const char*>(row) + l * 16);
-    if constexpr (sizeof(E) == 4)
-      fetch<16>(s + 512 + lane * 16, reinterpret_cast<const char*>(row) + D * 2 + l * 16);
+  __device__ __forceinline__ static void ask(char* s, const char* from, int lane) {
+    fetch<16>(s + lane * 16, from);
+    if constexpr (sizeof(E) == 4) fetch<16>(s + 512 + lane * 16, from + D * 2);
   }
   __device__ __forceinline__ static Raw<E> get(const char* s, int lane) {
     Raw<E> r;
@@ -121,6 +118,15 @@ struct Slot {
     }
     return r;
   }
+  // `to` is where the lane's first 16 bytes go
+  __device__ __forceinline__ static void put(char* to, const Raw<E>& r) {
+    if constexpr (sizeof(E) == 2) {
+      *reinterpret_cast<uint4*>(to) = r.u;
+    } else {
+      *reinterpret_cast<float4*>(to) = r.a;
+      *reinterpret_cast<float4*>(to + D * 2) = r.b;
+    }
+  }
 };
 
 // T rows of codes (raw q, k and, if T = 3, v of a token and head) and their
@@ -130,21 +136,28 @@ struct Slot {
 // wait and its reads, and between those and the next copies.
 template <typename E, int D, int T, bool TwoHeads>
 struct CodeRows {
-  static constexpr int G = D / 8, R = 32 / G;
+  static constexpr int G = D / 8, R = 32 / G, kVec = TwoHeads ? 16 : 8;
   static constexpr int kScales = T * 512, kBytes = kScales + 2 * R * T * 4;
-  __device__ __forceinline__ static void ask(char* s, const int8_t* codes, const float* scales,
-                                             int n, int h, int n_h, int u, int sub, int l) {
+  // the lane's pointers for head h: codes of kind i, and the scale of kind l
+  __device__ __forceinline__ static const char* codes_at(const int8_t* codes, int i, int h,
+                                                         int n_h, int l) {
+    return reinterpret_cast<const char*>(codes) + ((long long)i * n_h + h) * D + l * kVec;
+  }
+  __device__ __forceinline__ static const float* scale_at(const float* scales, int h, int n_h,
+                                                          int l) {
+    return scales + min(l, T - 1) * n_h + h;
+  }
+  __device__ __forceinline__ static void ask(char* s, const char* const (&codes)[T],
+                                             const float* scale, int n, int n_h, int u, int sub,
+                                             int l) {
     if (TwoHeads && u == 1) return;
+    const uint32_t stride = 3 * n_h;
 #pragma unroll
-    for (int i = 0; i < T; ++i) {
-      const int8_t* row = at_bytes(codes, (n * 3 + i) * n_h + h, D);
-      if constexpr (TwoHeads)
-        fetch<16>(s + i * 512 + (sub * G + l) * 16, row + l * 16);
-      else
-        fetch<8>(s + i * 512 + u * 256 + (sub * G + l) * 8, row + l * 8);
-    }
+    for (int i = 0; i < T; ++i)
+      fetch<kVec>(s + i * 512 + (TwoHeads ? 0 : u * 256) + (sub * G + l) * kVec,
+                  at_bytes(codes[i], n, stride * D));
     if (l < T) {
-      const float* from = scales + (uint32_t)((n * 3 + l) * n_h + h);
+      const float* from = at_bytes(scale, n, stride * 4);
       float* to = reinterpret_cast<float*>(s + kScales);
       if constexpr (TwoHeads)
         fetch<8>(to + (sub * T + l) * 2, from);
@@ -163,17 +176,6 @@ struct CodeRows {
     return TwoHeads ? p[(sub * T + i) * 2 + u] : p[(u * R + sub) * T + i];
   }
 };
-
-template <int D>
-__device__ __forceinline__ void store_raw(__nv_bfloat16* row, int l, const Raw<__nv_bfloat16>& r) {
-  reinterpret_cast<uint4*>(row)[l] = r.u;
-}
-template <int D>
-__device__ __forceinline__ void store_raw(float* row, int l, const Raw<float>& r) {
-  float4* p = reinterpret_cast<float4*>(row);
-  p[l] = r.a;
-  p[D / 8 + l] = r.b;
-}
 
 // A lane's eight values as four adjacent pairs: fp32 arithmetic runs on pairs
 // (two lanes of one instruction each), and a rotation turns one.
@@ -337,29 +339,27 @@ __device__ __forceinline__ float max_abs3(float a, float b, float c) {
 // pair of significands); with 254 / 128 each value is settled exactly.
 // fp32: where a quotient's distance from its integer is so close to a half
 // that the factor's error could decide, the lane settles its eight.
+// A group with a outside [2^-119, 2^100] (nothing to scale, not finite, or
+// with a subnormal reciprocal) goes the settling way too.
 template <typename E>
 __device__ __forceinline__ uint2 encode8(const Vals& v, uint32_t m, float& scale) {
   const float a = __uint_as_float(m);
-  const bool bad = m >= 0x7F800000u, none = a < 0x1p-119f;
   // a / 127 correctly rounded: a first quotient and one step with its exact
   // remainder (Markstein's division; checked against a / 127 for every mantissa)
   constexpr float kInv = 1.0f / 127.0f;
   const float q = a * kInv;
   scale = fmaf(fmaf(-127.0f, q, a), kInv, q);
-  scale = bad ? __uint_as_float(0x7FC00000u) : (none ? 0.f : scale);
-  // a large a is scaled down, so that its reciprocal stays normal
-  constexpr float kTop = sizeof(E) == 2 ? 127.0f * (1.0f + 0x1p-19f) : 127.0f;
-  const bool large = a > 0x1p100f;
   float inv;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(large ? a * 0x1p-8f : a));
-  inv *= large ? kTop * 0x1p-8f : kTop;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(a));
+  inv *= sizeof(E) == 2 ? 127.0f * (1.0f + 0x1p-19f) : 127.0f;
   constexpr float kMagic = 12582912.0f;
   Vals z;
 #pragma unroll
   for (int i = 0; i < 4; ++i) z.p[i] = __ffma2_rn(v.p[i], both(inv), both(kMagic));
-  bool close;
+  constexpr uint32_t kLow = 0x04000000u, kHigh = 0x71800000u;      // 2^-119, 2^100
+  bool rare = m - kLow > kHigh - kLow;
   if constexpr (sizeof(E) == 2) {
-    close = (m & 0x007F0000u) == 0x007E0000u;
+    rare = rare || (m & 0x007F0000u) == 0x007E0000u;
   } else {
     float border = 0.f;
 #pragma unroll
@@ -368,14 +368,19 @@ __device__ __forceinline__ uint2 encode8(const Vals& v, uint32_t m, float& scale
           __ffma2_rn(v.p[i], both(inv), __ffma2_rn(z.p[i], both(-1.f), both(kMagic)));
       border = max_abs3(border, d.x, d.y);
     }
-    close = border > 0.5f - 0x1p-14f;
+    rare = rare || border > 0.5f - 0x1p-14f;
   }
-  if (close) {
-    const float down = large ? 0x1p-8f : 1.0f;
+  if (rare) {
+    const bool bad = m >= 0x7F800000u, none = m < kLow;
+    if (bad) scale = __uint_as_float(0x7FC00000u);
+    if (none) scale = 0.f;
+    const float down = m > kHigh ? 0x1p-8f : 1.0f;
+    const float by = __fdividef(127.0f, a * down) * down;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float c = z.at(i) - kMagic;
-      z.at(i) = settle(v.at(i) * down, a * down, c, fmaf(v.at(i), inv, -c)) + kMagic;
+      const float c = rintf(v.at(i) * by);
+      const float code = settle(v.at(i) * down, a * down, c, fmaf(v.at(i), by, -c));
+      z.at(i) = bad || none ? kMagic : code + kMagic;
     }
   }
   uint32_t w[8];
@@ -385,7 +390,7 @@ __device__ __forceinline__ uint2 encode8(const Vals& v, uint32_t m, float& scale
                                   0x5410);
   const uint32_t hi = __byte_perm(__byte_perm(w[4], w[5], 0x0040), __byte_perm(w[6], w[7], 0x0040),
                                   0x5410);
-  return bad || none ? make_uint2(0u, 0u) : make_uint2(lo, hi);
+  return make_uint2(lo, hi);
 }
 
 // Eight codes as fp32.  A byte c + 128 in the mantissa of 2^23 is 2^23 + 128 + c.
@@ -411,15 +416,15 @@ __device__ __forceinline__ Vals decode8(uint2 c, float scale) {
   return scaled(code_values(c), scale);
 }
 
-// A lane's eight codes into a row of D codes, from the element order of E.
+// A lane's eight codes into a row of D codes, from the element order of E;
+// `to` is where its first go.
 template <typename E, int D>
-__device__ __forceinline__ void store_codes(int8_t* row, int l, uint2 c) {
+__device__ __forceinline__ void store_codes(char* to, uint2 c) {
   if (sizeof(E) == 2) {
-    reinterpret_cast<uint2*>(row)[l] = c;
+    *reinterpret_cast<uint2*>(to) = c;
   } else {
-    uint32_t* p = reinterpret_cast<uint32_t*>(row);
-    p[l] = c.x;
-    p[D / 8 + l] = c.y;
+    *reinterpret_cast<uint32_t*>(to) = c.x;
+    *reinterpret_cast<uint32_t*>(to + D / 2) = c.y;
   }
 }
 
