@@ -77,6 +77,11 @@ struct Smem {
   static constexpr int kBytes = kRing + kSpots + 16 * kLanes * (int)sizeof(double);
 };
 
+// n strides and so many bytes more.
+__device__ __forceinline__ unsigned long long offset(int n, uint32_t stride, uint32_t more) {
+  return (unsigned long long)(uint32_t)n * stride + more;
+}
+
 template <typename E, int D, bool From8, bool TwoHeads>
 __global__ void __launch_bounds__(kThreads, 2)
 k_norm_rope_bwd(const __grid_constant__ Walk w, const __grid_constant__ NormRopeArgs a,
@@ -153,19 +158,21 @@ k_norm_rope_bwd(const __grid_constant__ Walk w, const __grid_constant__ NormRope
           }
         }
         char* to = ring + stage * F::kBytes;
-        const long long more = (ahead.h0 + (TwoHeads ? u : 0)) * (long long)(D * sizeof(E));
-        Slot<E, D>::ask(to + 3 * u * F::kSlot, at_bytes(in_dq, n, row3) + more, lane);
-        Slot<E, D>::ask(to + (3 * u + 1) * F::kSlot, at_bytes(in_dk, n, row3) + more, lane);
-        Slot<E, D>::ask(to + (3 * u + 2) * F::kSlot, at_bytes(in_dv, n, row3) + more, lane);
+        constexpr int kHead = D * sizeof(E);
+        const uint32_t first = ahead.h0 * kHead, more = TwoHeads ? u * kHead : 0;
+        const unsigned long long at = offset(n, row3, first);
+        Slot<E, D>::ask(to + 3 * u * F::kSlot, in_dq + at + more, lane);
+        Slot<E, D>::ask(to + (3 * u + 1) * F::kSlot, in_dk + at + more, lane);
+        Slot<E, D>::ask(to + (3 * u + 2) * F::kSlot, in_dv + at + more, lane);
         to += F::kRaw;
         if constexpr (From8) {
-          const char* const codes[2] = {in_raw[0] + (long long)ahead.h0 * D,
-                                        in_raw[1] + (long long)ahead.h0 * D};
+          const char* const codes[2] = {in_raw[0] + ahead.h0 * D, in_raw[1] + ahead.h0 * D};
           F::C::ask(to, codes, in_scale + ahead.h0, n, w.n_h, u, sub, l);
         } else {
+          const unsigned long long raw = offset(n, w.ld, first);
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            Slot<E, D>::ask(to + (2 * u + i) * F::kSlot, at_bytes(in_raw[i], n, w.ld) + more, lane);
+            Slot<E, D>::ask(to + (2 * u + i) * F::kSlot, in_raw[i] + raw + more, lane);
         }
       }
       ahead.n0 += kStride;
@@ -199,7 +206,11 @@ k_norm_rope_bwd(const __grid_constant__ Walk w, const __grid_constant__ NormRope
           load_turns(refs, a.table, w.still, spot, cs[u]);
         }
       }
-      const int h0 = cur.h0;
+      unsigned long long out[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        out[u] = TwoHeads && u ? out[0] + D * sizeof(E)
+                               : offset(n[u], w.ld_out, cur.h0 * (int)(D * sizeof(E)));
       fetch_wait<S - 1>();
       if constexpr (From8) __syncwarp();
       const char* in = ring + stage * F::kBytes;
@@ -207,9 +218,7 @@ k_norm_rope_bwd(const __grid_constant__ Walk w, const __grid_constant__ NormRope
 #pragma unroll
       for (int u = 0; u < 2; ++u)
         if (mine[u])
-          Slot<E, D>::put(at_bytes(to_v, n[u], w.ld_out) +
-                              (h0 + (TwoHeads ? u : 0)) * (long long)(D * sizeof(E)),
-                          F::grad(in, 2, u, lane));
+          Slot<E, D>::put(to_v + out[u], F::grad(in, 2, u, lane));
       Vals x[4];
       float r[4], dot[4];
       F::load(in, a.eps, sub, l, x, r);          // xh = x r
@@ -235,9 +244,7 @@ k_norm_rope_bwd(const __grid_constant__ Walk w, const __grid_constant__ NormRope
         if (mine[k / 2]) {
           Raw<E> s;
           pack(g[k], s);
-          Slot<E, D>::put(at_bytes(k & 1 ? to_k : to_q, n[k / 2], w.ld_out) +
-                              (h0 + (TwoHeads ? k / 2 : 0)) * (long long)(D * sizeof(E)),
-                          s);
+          Slot<E, D>::put((k & 1 ? to_k : to_q) + out[k / 2], s);
         }
       }
     }
