@@ -70,6 +70,7 @@ k_act8_pack(const E* __restrict__ x, const __grid_constant__ Shape s, int8_t* __
   const int most = (int)min(s.n_groups - base, (long long)(kUnroll * kPer));
   Raw<E> r[kUnroll];
   Place at[kUnroll];
+  after_previous();
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
     const int k = u * kPer + threadIdx.x / G;
@@ -130,6 +131,7 @@ k_act8_unpack(const int8_t* __restrict__ codes, const float* __restrict__ scales
   uint2 w[kUnroll];
   float scale[kUnroll];
   Place at[kUnroll];
+  after_previous();
 #pragma unroll
   for (int u = 0; u < kUnroll; ++u) {
     const int k = min(u * kPer + (int)threadIdx.x / G, most - 1);
@@ -196,12 +198,8 @@ cudaError_t pack_t(const void* x, long long n_rows, int cols, long long ld, int8
   const Shape s = shape_of<Group>(n_rows, cols, ld, &ctas);
   const auto kernel = vectors<E>(x, ld, cols, codes) ? k_act8_pack<E, Group, true>
                                                      : k_act8_pack<E, Group, false>;
-  {
-    VMOBA_TRACE("k_act8_pack", st);
-    kernel<<<ctas, kThreads, 0, st>>>(static_cast<const E*>(x), s, codes, scales);
-  }
-  count_launches(1);
-  return cudaGetLastError();
+  VMOBA_TRACE("k_act8_pack", st);
+  return launch(kernel, dim3(ctas), kThreads, 0, 1, st, static_cast<const E*>(x), s, codes, scales);
 }
 
 template <typename E, int Group>
@@ -211,12 +209,8 @@ cudaError_t unpack_t(const int8_t* codes, const float* scales, long long n_rows,
   const Shape s = shape_of<Group>(n_rows, cols, ld, &ctas);
   const auto kernel = vectors<E>(out, ld, cols, codes) ? k_act8_unpack<E, Group, true>
                                                        : k_act8_unpack<E, Group, false>;
-  {
-    VMOBA_TRACE("k_act8_unpack", st);
-    kernel<<<ctas, kThreads, 0, st>>>(codes, scales, s, static_cast<E*>(out));
-  }
-  count_launches(1);
-  return cudaGetLastError();
+  VMOBA_TRACE("k_act8_unpack", st);
+  return launch(kernel, dim3(ctas), kThreads, 0, 1, st, codes, scales, s, static_cast<E*>(out));
 }
 
 }  // namespace

@@ -149,6 +149,7 @@ k_norm_rope(const __grid_constant__ Walk w, const __grid_constant__ NormRopeArgs
   const int first = (blockIdx.x - j * w.chunks) * w.chunk, last = min(first + w.chunk, w.L);
   const int step = kWarps / w.up * R;
 
+  after_previous();
   const Vals gq = load_weights<E, D>(a.gq, l), gk = load_weights<E, D>(a.gk, l);
   const PairRefs refs = pair_refs<E, D>(l, a.ht, a.hh, a.hw);
   const int y_rows = w.T * a.ht, x_rows = y_rows + w.H * a.hh;
@@ -419,23 +420,9 @@ cudaError_t launch_t(const Prob& P, const NormRopeArgs& a, const NormRopeOut& o,
   }
   w.hw = FastDiv(w.bh * w.bw);
   w.w = FastDiv(w.bw);
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(w.Nb * w.chunks, units / w.up);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = M::kBytes;
-  cfg.stream = st;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = o.blocks ? w.chunks : 1;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  {
-    VMOBA_TRACE("k_norm_rope", st);
-    e = cudaLaunchKernelEx(&cfg, kernel, w, a, o);
-  }
-  count_launches(1);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  VMOBA_TRACE("k_norm_rope", st);
+  return launch(kernel, dim3(w.Nb * w.chunks, units / w.up), kThreads, M::kBytes,
+                o.blocks ? w.chunks : 1, st, w, a, o);
 }
 
 template <typename E, int D, bool TwoHeads>
@@ -459,6 +446,7 @@ cudaError_t launch_d(const Prob& P, const NormRopeArgs& a, const NormRopeOut& o,
 __global__ void k_rope_table(int T, int H, int W, int ht, int hh, int hw, double base,
                              long long ot, long long oy, long long ox, float2* table) {
   const int nt = T * ht, ny = H * hh, nx = W * hw;
+  after_previous();
   const int i = blockIdx.x * blockDim.x + threadIdx.x;
   if (i >= nt + ny + nx) return;
   const int k = i < nt ? i : (i < nt + ny ? i - nt : i - nt - ny);
@@ -485,13 +473,9 @@ cudaError_t launch_rope_table(int T, int H, int W, int ht, int hh, int hw, doubl
                               const long long (&origin)[3], float2* table, cudaStream_t st) {
   const int n = T * ht + H * hh + W * hw;
   if (n == 0) return cudaSuccess;
-  {
-    VMOBA_TRACE("k_rope_table", st);
-    k_rope_table<<<(n + 127) / 128, 128, 0, st>>>(T, H, W, ht, hh, hw, base, origin[0], origin[1],
-                                                  origin[2], table);
-  }
-  count_launches(1);
-  return cudaGetLastError();
+  VMOBA_TRACE("k_rope_table", st);
+  return launch(k_rope_table, dim3((n + 127) / 128), 128, 0, 1, st, T, H, W, ht, hh, hw, base,
+                origin[0], origin[1], origin[2], table);
 }
 
 }  // namespace vmoba

@@ -98,6 +98,7 @@ k_norm_rope_bwd(const __grid_constant__ Walk w, const __grid_constant__ NormRope
   Spot* spots = reinterpret_cast<Spot*>(smem + M::kRing) + warp * (S * 8);
   double(&sums)[16][M::kLanes] =
       *reinterpret_cast<double(*)[16][M::kLanes]>(smem + M::kRing + M::kSpots);
+  after_previous();
   const Vals gq = load_weights<E, D>(a.gq, l), gk = load_weights<E, D>(a.gk, l);
   const PairRefs refs = pair_refs<E, D>(l, a.ht, a.hh, a.hw);
   const int y_rows = w.T * a.ht, x_rows = y_rows + w.H * a.hh;
@@ -280,6 +281,7 @@ __global__ void __launch_bounds__(1024)
 k_norm_dweight(const float* __restrict__ part, int n, int cols, float* __restrict__ out) {
   __shared__ double sums[32][33];
   const int c = threadIdx.x & 31, k = threadIdx.x >> 5;
+  after_previous();
   const float* p = part + blockIdx.x * 32 + c;
   double sum = 0.0;
 #pragma unroll 8
@@ -322,19 +324,14 @@ cudaError_t launch_t(const Prob& P, const NormRopeArgs& a, const void* dq, const
   if (e != cudaSuccess) return e;
   {
     VMOBA_TRACE("k_norm_rope_bwd", st);
-    kernel<<<ctas, kThreads, smem, st>>>(
-        w, a, static_cast<const E*>(dq), static_cast<const E*>(dk), static_cast<const E*>(dv),
-        static_cast<E*>(out[0]), static_cast<E*>(out[1]), static_cast<E*>(out[2]), part);
+    e = launch(kernel, dim3(ctas), kThreads, smem, 1, st, w, a, static_cast<const E*>(dq),
+               static_cast<const E*>(dk), static_cast<const E*>(dv), static_cast<E*>(out[0]),
+               static_cast<E*>(out[1]), static_cast<E*>(out[2]), part);
   }
-  count_launches(1);
-  e = cudaGetLastError();
   if (e != cudaSuccess || !dweight) return e;
-  {
-    VMOBA_TRACE("k_norm_dweight", st);
-    k_norm_dweight<<<2 * D / 32, 1024, 0, st>>>(part, ctas, 2 * D, dweight);
-  }
-  count_launches(1);
-  return cudaGetLastError();
+  VMOBA_TRACE("k_norm_dweight", st);
+  return launch(k_norm_dweight, dim3(2 * D / 32), 1024, 0, 1, st, static_cast<const float*>(part),
+                ctas, 2 * D, dweight);
 }
 
 }  // namespace

@@ -270,6 +270,14 @@ __device__ __forceinline__ float lane_dot(const Vals& a, const Vals& b) {
   return s.x + s.y;
 }
 
+// Waits until the stream's previous kernel has finished and its writes are
+// visible (every access to global memory comes after this), and lets the next
+// one be set up once all of this grid's CTAs run.
+__device__ __forceinline__ void after_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ---- 8-bit groups ----
 
 // Group maxima of |x| as bits: an infinity or NaN sorts above every finite
@@ -590,6 +598,29 @@ __device__ __forceinline__ Vals load_weights(const float* g, int l) {
 }
 
 }  // namespace rows
+
+// Launches a kernel that begins with after_previous(): it may be set up while
+// the stream's previous kernel still runs its last CTAs.
+template <typename K, typename... A>
+cudaError_t launch(K kernel, dim3 grid, int block, int smem, int cluster, cudaStream_t st,
+                   const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2]{};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  count_launches(1);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
 
 // A kernel's opt-in to more than 48 KB of shared memory, once per device.
 class SmemOptIn {
