@@ -121,10 +121,10 @@ struct Slot {
   // `to` is where the lane's first 16 bytes go
   __device__ __forceinline__ static void put(char* to, const Raw<E>& r) {
     if constexpr (sizeof(E) == 2) {
-      *reinterpret_cast<uint4*>(to) = r.u;
+      __stcg(reinterpret_cast<uint4*>(to), r.u);
     } else {
-      *reinterpret_cast<float4*>(to) = r.a;
-      *reinterpret_cast<float4*>(to + D * 2) = r.b;
+      __stcg(reinterpret_cast<float4*>(to), r.a);
+      __stcg(reinterpret_cast<float4*>(to + D * 2), r.b);
     }
   }
 };
@@ -429,10 +429,10 @@ __device__ __forceinline__ Vals decode8(uint2 c, float scale) {
 template <typename E, int D>
 __device__ __forceinline__ void store_codes(char* to, uint2 c) {
   if (sizeof(E) == 2) {
-    *reinterpret_cast<uint2*>(to) = c;
+    __stcg(reinterpret_cast<uint2*>(to), c);
   } else {
-    *reinterpret_cast<uint32_t*>(to) = c.x;
-    *reinterpret_cast<uint32_t*>(to + D / 2) = c.y;
+    __stcg(reinterpret_cast<uint32_t*>(to), c.x);
+    __stcg(reinterpret_cast<uint32_t*>(to + D / 2), c.y);
   }
 }
 
