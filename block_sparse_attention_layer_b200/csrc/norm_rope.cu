@@ -145,8 +145,10 @@ k_norm_rope(const __grid_constant__ Walk w, const __grid_constant__ NormRopeArgs
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane / G, l = lane % G;
   const int h0 = (blockIdx.y * w.up + warp % w.up) * NA;
-  const int j = blockIdx.x / w.chunks;
-  const int first = (blockIdx.x - j * w.chunks) * w.chunk, last = min(first + w.chunk, w.L);
+  // partition order: chunk x of block z; token order: chunk z
+  const int j = o.blocks ? blockIdx.z : 0;
+  const int first = (o.blocks ? blockIdx.x : blockIdx.z) * w.chunk;
+  const int last = min(first + w.chunk, w.L);
   const int step = kWarps / w.up * R;
 
   after_previous();
@@ -421,8 +423,11 @@ cudaError_t launch_t(const Prob& P, const NormRopeArgs& a, const NormRopeOut& o,
   w.hw = FastDiv(w.bh * w.bw);
   w.w = FastDiv(w.bw);
   VMOBA_TRACE("k_norm_rope", st);
-  return launch(kernel, dim3(w.Nb * w.chunks, units / w.up), kThreads, M::kBytes,
-                o.blocks ? w.chunks : 1, st, w, a, o);
+  // all heads of neighbouring tokens run at one time: whole rows of DRAM pages
+  const int groups = units / w.up;
+  return o.blocks ? launch(kernel, dim3(w.chunks, groups, w.Nb), kThreads, M::kBytes, w.chunks,
+                           st, w, a, o)
+                  : launch(kernel, dim3(1, groups, w.chunks), kThreads, M::kBytes, 1, st, w, a, o);
 }
 
 template <typename E, int D, bool TwoHeads>

@@ -31,7 +31,7 @@ struct Walk {
   int chunk, still;                // tokens of a work item; whether some pairs do not turn
   FastDiv hw, w;                   // H * W, W
   uint32_t ld, ld_out;             // bytes between tokens
-  int n_items, n_chunks;
+  int n_items, units;              // units of heads
 };
 
 // The gradients and the raw q and k of two rows on their way through shared
@@ -115,7 +115,7 @@ k_norm_rope_bwd(const __grid_constant__ Walk w, const __grid_constant__ NormRope
   };
   auto enter = [&](At& p) {          // the warp's first token of the item
     if (p.item >= w.n_items) return;
-    const int unit = p.item / w.n_chunks, c0 = (p.item - unit * w.n_chunks) * w.chunk;
+    const int c = p.item / w.units, unit = p.item - c * w.units, c0 = c * w.chunk;
     p.h0 = unit * (TwoHeads ? 2 : 1);
     p.n0 = c0 + warp * R;
     p.last = min(c0 + w.chunk, w.s);
@@ -310,8 +310,8 @@ cudaError_t launch_t(const Prob& P, const NormRopeArgs& a, const void* dq, const
   const int units = TwoHeads ? P.n_h / 2 : P.n_h, slots = min(2 * num_sms, kMaxCtas);
   const long long share = (long long)P.s * units / slots / stride;
   w.chunk = stride * (int)max(1LL, min(16LL, share));
-  w.n_chunks = (P.s + w.chunk - 1) / w.chunk;
-  w.n_items = w.n_chunks * units;
+  w.units = units;
+  w.n_items = (P.s + w.chunk - 1) / w.chunk * units;
   w.still = 2 * (a.ht + a.hh + a.hw) < D;
   const int ctas = min(w.n_items, slots);
   float* part = dweight ? static_cast<float*>(ws) : nullptr;
