@@ -74,7 +74,8 @@ struct Smem {
   static constexpr int kRing = kStages * kWarps * Feed<E, D, From8, TwoHeads>::kBytes;
   static constexpr int kSpots = kStages * kWarps * 8 * (int)sizeof(Spot);
   static constexpr int kLanes = kWarps * (D / 8);      // lanes of one row in every warp
-  static constexpr int kBytes = kRing + kSpots + 16 * kLanes * (int)sizeof(double);
+  static constexpr int kBytes =
+      kRing + kSpots + 16 * kLanes * (int)sizeof(double) + 2 * D * (int)sizeof(float);
 };
 
 // n strides and so many bytes more.
@@ -98,8 +99,10 @@ k_norm_rope_bwd(const __grid_constant__ Walk w, const __grid_constant__ NormRope
   Spot* spots = reinterpret_cast<Spot*>(smem + M::kRing) + warp * (S * 8);
   double(&sums)[16][M::kLanes] =
       *reinterpret_cast<double(*)[16][M::kLanes]>(smem + M::kRing + M::kSpots);
+  float* g_smem = reinterpret_cast<float*>(&sums[16][0]);
   after_previous();
-  const Vals gq = load_weights<E, D>(a.gq, l), gk = load_weights<E, D>(a.gk, l);
+  for (int c = threadIdx.x; c < 2 * D; c += kThreads) place_weight<E, D>(a, c, g_smem);
+  __syncthreads();
   const PairRefs refs = pair_refs<E, D>(l, a.ht, a.hh, a.hw);
   const int y_rows = w.T * a.ht, x_rows = y_rows + w.H * a.hh;
   const uint32_t row3 = w.n_h * D * sizeof(E);
@@ -229,10 +232,11 @@ k_norm_rope_bwd(const __grid_constant__ Walk w, const __grid_constant__ NormRope
         g[k] = unpack(F::grad(in, k & 1, k / 2, lane));
         turn_back(g[k], cs[TwoHeads ? 0 : k / 2]);
         Vals& sum = k & 1 ? wk : wq;
+        const Vals weight = weights<D>(g_smem + (k & 1) * D, l);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if (mine[k / 2]) sum.p[i] = __ffma2_rn(g[k].p[i], x[k].p[i], sum.p[i]);
-          g[k].p[i] = __fmul2_rn(g[k].p[i], k & 1 ? gk.p[i] : gq.p[i]);
+          g[k].p[i] = __fmul2_rn(g[k].p[i], weight.p[i]);
         }
         dot[k] = lane_dot(g[k], x[k]);
       }

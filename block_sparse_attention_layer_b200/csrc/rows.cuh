@@ -20,6 +20,9 @@
 #include "common.cuh"
 
 namespace vmoba {
+
+struct NormRopeArgs;
+
 namespace rows {
 
 constexpr unsigned kAll = 0xFFFFFFFFu;
@@ -597,6 +600,18 @@ __device__ __forceinline__ Vals load_weights(const float* g, int l) {
   return w;
 }
 
+// The weights of q and k (2 D) in shared memory: a lane's first four and last
+// four elements lie in separate halves (16-byte reads without bank conflicts).
+template <typename E, int D>
+__device__ __forceinline__ void place_weight(const NormRopeArgs& a, int c, float* to);
+template <int D>
+__device__ __forceinline__ Vals weights(const float* g, int l) {
+  const float4 a = reinterpret_cast<const float4*>(g)[l];
+  const float4 b = reinterpret_cast<const float4*>(g + D / 2)[l];
+  return {make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y),
+          make_float2(b.z, b.w)};
+}
+
 }  // namespace rows
 
 // Launches a kernel that begins with after_previous(): it may be set up while
@@ -647,6 +662,15 @@ struct NormRopeArgs {
   const float2* table;        // (cos, sin): T * ht, then H * hh, then W * hw entries
   int ht, hh, hw;             // pairs that turn with t, y, x
 };
+
+namespace rows {
+template <typename E, int D>
+__device__ __forceinline__ void place_weight(const NormRopeArgs& a, int c, float* to) {
+  const float* g = c < D ? a.gq : a.gk;
+  const int half = c % D / (D / 2), l = c % (D / 2) / 4;
+  to[c] = g ? __ldg(g + elem_at<E, D>(l, half * 4 + c % 4)) : 1.f;
+}
+}  // namespace rows
 
 struct NormRopeOut {
   void *q, *k, *v;
