@@ -346,6 +346,7 @@ int norm_rope_args(const Prob& P, const vmoba_norm_rope* nr, NormRopeArgs* a) {
   n.gq = nr->q_weight; n.gk = nr->k_weight; n.eps = nr->eps;
   n.table = reinterpret_cast<const float2*>(nr->table);
   n.ht = nr->dim_t / 2; n.hh = nr->dim_h / 2; n.hw = nr->dim_w / 2;
+  n.still = nr->dim_t + nr->dim_h + nr->dim_w < P.d;
   *a = n;
   return VMOBA_OK;
 }

@@ -40,7 +40,6 @@ struct Walk {
   FastDiv hw, w;                   // bh * bw, bw
   int chunk, chunks;               // rows of a chunk, chunks of a block
   int up;                          // units of heads of a CTA
-  int still;                       // whether some pairs do not turn
   uint32_t ld, q_tok, kv_tok;      // bytes between tokens of the raw rows and q; positions of k, v
   long long kv_head;               // elements between heads of k and v
 };
@@ -234,7 +233,7 @@ k_norm_rope(const __grid_constant__ Walk w, const __grid_constant__ NormRopeArgs
         mine[u] = r[u] < last;
         const Spot* spot = spots + stage * 8 + u * 4 + sub;
         n[u] = spot->n;
-        load_turns(refs, a.table, w.still, spot, cs[u]);
+        load_turns(refs, a.table, a.still, spot, cs[u]);
       }
     }
     fetch_wait<S - 1>();
@@ -384,15 +383,21 @@ cudaError_t launch_t(const Prob& P, const NormRopeArgs& a, const NormRopeOut& o,
   w.nbh = P.nbh; w.nbw = P.nbw; w.Nb = P.Nb; w.L = P.L;
   w.ld = (uint32_t)(a.ld * sizeof(E));
   w.q_tok = P.n_h * D * sizeof(E);
-  w.still = 2 * (a.ht + a.hh + a.hw) < D;
   if (o.blocks) {
     w.kv_tok = D * sizeof(E);
     w.kv_head = (long long)P.s * D;
-    // the units and chunks of a CTA for which the slowest of the places that
-    // CTAs run in has the fewest steps; a CTA's filling and reducing costs
-    // about two
+    // One CTA for each block and unit of heads where these are at least one and
+    // a half rounds of CTAs (1.6 rounds: 108 us against 113 of the search
+    // below on 32760 tokens in 78 blocks; 5.8 rounds: 162 against 165 on 55296
+    // tokens in 288 blocks; but from codes 141 against 137).  Else the units and chunks of a CTA for which the
+    // slowest of the places that CTAs run in has the fewest steps, a CTA's
+    // filling and reducing costing about two (55296 tokens in 8 blocks: 179 us
+    // against 187 with eight chunks of two units, 433 with one CTA a block).
+    w.up = w.chunks = 1;
     long long best = -1;
-    for (int up = units % 2 == 0 ? 2 : 1; up >= 1; --up) {
+    const bool many = !From8 && 2LL * P.Nb * units >=
+                                    3LL * capacity.ctas(kernel, dev, 1, M::kBytes, num_sms);
+    for (int up = units % 2 == 0 ? 2 : 1; up >= 1 && !many; --up) {
       const int step = kWarps / up * R;
       for (int c = 1; c <= 8 && c <= P.L; ++c) {
         const long long ctas = (long long)P.Nb * c * (units / up);

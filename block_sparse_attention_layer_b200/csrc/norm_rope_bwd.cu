@@ -28,7 +28,7 @@ constexpr int kMaxCtas = 1024;      // partial weight gradients in the workspace
 
 struct Walk {
   int T, H, W, s, n_h;
-  int chunk, still;                // tokens of a work item; whether some pairs do not turn
+  int chunk;                       // tokens of a work item
   FastDiv hw, w;                   // H * W, W
   uint32_t ld, ld_out;             // bytes between tokens
   int n_items, units;              // units of heads
@@ -207,7 +207,7 @@ k_norm_rope_bwd(const __grid_constant__ Walk w, const __grid_constant__ NormRope
           mine[u] = cur.n0 + u * kStep + sub < cur.last;
           const Spot* spot = spots + stage * 8 + u * 4 + sub;
           n[u] = spot->n;
-          load_turns(refs, a.table, w.still, spot, cs[u]);
+          load_turns(refs, a.table, a.still, spot, cs[u]);
         }
       }
       unsigned long long out[2];
@@ -308,15 +308,22 @@ cudaError_t launch_t(const Prob& P, const NormRopeArgs& a, const void* dq, const
   w.w = FastDiv(P.W);
   w.ld = (uint32_t)(a.ld * sizeof(E));
   w.ld_out = (uint32_t)(ld_out * sizeof(E));
-  // items of one stride of the CTA's warps up to sixteen, so that two CTAs on
-  // every SM have one where the tokens suffice
+  // items of up to 32 strides of the CTA's warps, of the length for which the
+  // CTA with the most items has the fewest strides (55296 tokens of 12 heads:
+  // four items of 18 where 4.4 of 16 left a tenth of the CTAs' time unused)
   constexpr int stride = kWarps * (256 / D) * (TwoHeads ? 1 : 2);
   const int units = TwoHeads ? P.n_h / 2 : P.n_h, slots = min(2 * num_sms, kMaxCtas);
-  const long long share = (long long)P.s * units / slots / stride;
-  w.chunk = stride * (int)max(1LL, min(16LL, share));
+  const long long strides = (P.s + stride - 1) / stride;
+  long long best = -1;
+  for (int k = 32; k >= 1; --k) {
+    const long long items = (strides + k - 1) / k * units, most = (items + slots - 1) / slots * k;
+    if (best < 0 || most < best) {
+      best = most;
+      w.chunk = k * stride;
+    }
+  }
   w.units = units;
   w.n_items = (P.s + w.chunk - 1) / w.chunk * units;
-  w.still = 2 * (a.ht + a.hh + a.hw) < D;
   const int ctas = min(w.n_items, slots);
   float* part = dweight ? static_cast<float*>(ws) : nullptr;
   const auto kernel = k_norm_rope_bwd<E, D, From8, TwoHeads>;

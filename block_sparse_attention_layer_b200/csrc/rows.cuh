@@ -661,6 +661,7 @@ struct NormRopeArgs {
   float eps;
   const float2* table;        // (cos, sin): T * ht, then H * hh, then W * hw entries
   int ht, hh, hw;             // pairs that turn with t, y, x
+  bool still;                 // whether some pairs do not turn (the table has nothing for them)
 };
 
 namespace rows {
