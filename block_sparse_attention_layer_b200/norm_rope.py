@@ -9,7 +9,6 @@ device, which is made current during the call.
 from __future__ import annotations
 
 import ctypes
-import functools
 from dataclasses import dataclass
 
 import torch
@@ -136,55 +135,52 @@ def _ckpt(c: Act8, size, group, device, name):
 
 def _dims(shape: LayerShape, dims) -> tuple:
     """(dims, table rows), checked."""
-    try:
-        return _checked_dims(shape.T, shape.H, shape.W, shape.head_dim, dims)
-    except TypeError:               # a list cannot be looked up
-        return _checked_dims(shape.T, shape.H, shape.W, shape.head_dim, tuple(dims))
-
-
-@functools.lru_cache(maxsize=256)
-def _checked_dims(T, H, W, head_dim, dims):
-    ok = isinstance(dims, tuple) and len(dims) == 3 and all(isinstance(n, int) for n in dims)
-    if not ok or min(dims) < 0 or any(n & 1 for n in dims) or sum(dims) > head_dim:
-        raise ValueError(f"dims: expected three even numbers >= 0 of sum <= {head_dim}, got {dims}")
+    ok = isinstance(dims, (tuple, list)) and len(dims) == 3 and \
+        all(isinstance(n, int) for n in dims)
+    if not ok or min(dims) < 0 or any(n & 1 for n in dims) or sum(dims) > shape.head_dim:
+        raise ValueError(f"dims: expected three even numbers >= 0 of sum <= {shape.head_dim}, "
+                         f"got {dims}")
     t, h, w = dims
-    return t, h, w, (T * t + H * h + W * w) // 2
+    return t, h, w, (shape.T * t + shape.H * h + shape.W * w) // 2
 
 
 def _norm(shape: LayerShape, nr: NormRope, device):
-    """The norm and rotation as the ABI takes them."""
-    t, h, w, rows = _dims(shape, nr.dims)
-    gq, gk, table, d = nr.q_weight, nr.k_weight, 0, (shape.head_dim,)
-    if gq is not None:
-        gq = _at(gq, d, _F32, device, "q_weight")
-    if gk is not None:
-        gk = _at(gk, d, _F32, device, "k_weight")
-    if rows:
-        if nr.table is None:
-            raise ValueError("table: expected a rotation table (rope_table)")
-        table = _at(nr.table, (rows, 2), _F32, device, "table")
-    # the structure is built again only if a tensor's memory has moved
-    at = (gq, gk, table)
+    """The norm and rotation as the ABI takes them.  nr's tensors are checked
+    when they are first used with the shape, and again once one's memory has
+    moved; what they hold is read by each call's kernels."""
+    gq, gk, table = nr.q_weight, nr.k_weight, nr.table
+    at = (shape, device, gq if gq is None else gq.data_ptr(), gk if gk is None else gk.data_ptr(),
+          table if table is None else table.data_ptr())
     made = nr.__dict__.get("_made")
-    if made is None or made[0] != at:
-        made = at, ctypes.byref(CNormRope(gq, gk, nr.eps, table, t, h, w))
-        nr.__dict__["_made"] = made
-    return made[1]
+    if made is not None and made[0] == at:
+        return made[1]
+    t, h, w, rows = _dims(shape, nr.dims)
+    d = (shape.head_dim,)
+    g = [0 if x is None else _at(x, d, _F32, device, name)
+         for name, x in (("q_weight", gq), ("k_weight", gk))]
+    if rows and table is None:
+        raise ValueError("table: expected a rotation table (rope_table)")
+    c = ctypes.byref(CNormRope(*g, nr.eps, _at(table, (rows, 2), _F32, device, "table")
+                               if rows else 0, t, h, w))
+    nr.__dict__["_made"] = at, c
+    return c
 
 
-def _run(name, device, stream, *args) -> None:
+def _stream(device, stream) -> int:
     if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(device)
-    elif stream.device.index != device:
+        return torch._C._cuda_getCurrentRawStream(device)
+    if stream.device.index != device:
         raise ValueError(f"stream: expected one of cuda:{device}, got {stream.device}")
-    else:
-        stream = stream.cuda_stream
+    return stream.cuda_stream
+
+
+def _run(name, device, *args) -> None:
     fn = getattr(_lib._LIB or _lib.lib(), name)
     if device == torch._C._cuda_getDevice():
-        rc = fn(*args, stream)
+        rc = fn(*args)
     else:
         with torch.cuda.device(device):
-            rc = fn(*args, stream)
+            rc = fn(*args)
     if rc:
         _lib._check(name, rc)
 
@@ -198,27 +194,22 @@ def rope_table(shape: LayerShape, dims, base: float = 10000.0, origin=(0, 0, 0),
     positions counted from ``origin`` (a chunk of a longer video)."""
     t, h, w, rows = _dims(shape, dims)
     table = torch.empty((rows, 2), dtype=_F32, device=device)
-    _run("vmoba_rope_table", _device(table, "table"), stream, shape._ref, t, h, w, float(base),
-         *(int(o) for o in origin), table.data_ptr())
+    on = _device(table, "table")
+    _run("vmoba_rope_table", on, shape._ref, t, h, w, float(base), *(int(o) for o in origin),
+         table.data_ptr(), _stream(on, stream))
     return table
 
 
-def _forward(name, shape, nr, qkv, q, k, v, kv_size, blocks, ckpt, stream):
-    token, _, raw, means, dtype = shape._sizes
-    device = _device(q, "q")
+def _source(shape, qkv, ckpt, device):
+    """The forward's leading arguments and the checkpoint's trailing ones."""
     if isinstance(qkv, Act8):
         if ckpt is not None:
             raise ValueError("ckpt: the raw values already come from a checkpoint")
-        name += "_act8"
-        src, more = _ckpt(qkv, raw, token[2], device, "qkv"), ()
-    else:
-        src = _raw(shape, qkv, device, "qkv")
-        more = (0, 0) if ckpt is None else _ckpt(ckpt, raw, token[2], device, "ckpt")
-    out = (_at(q, token, dtype, device, "q"), _at(k, kv_size, dtype, device, "k"),
-           _at(v, kv_size, dtype, device, "v"))
-    if blocks is not None:
-        more = (_at(blocks, means, _F32, device, "blocks"), *more)
-    _run(name, device, stream, shape._ref, _norm(shape, nr, device), *src, *out, *more)
+        return _ckpt(qkv, shape._sizes[2], shape.head_dim, device, "qkv"), ()
+    if ckpt is None:
+        return _raw(shape, qkv, device, "qkv"), (0, 0)
+    return (_raw(shape, qkv, device, "qkv"),
+            _ckpt(ckpt, shape._sizes[2], shape.head_dim, device, "ckpt"))
 
 
 def qk_norm_rope(shape, nr, qkv, q, k, v, ckpt=None, stream=None) -> None:
@@ -227,7 +218,13 @@ def qk_norm_rope(shape, nr, qkv, q, k, v, ckpt=None, stream=None) -> None:
     [s][3][heads][d] (tokens any stride apart), three [s][heads][d] tensors, or
     an Act8 checkpoint of it; ckpt: an Act8 to store the raw rows in (groups
     of head_dim), in the same pass."""
-    _forward("vmoba_qk_norm_rope", shape, nr, qkv, q, k, v, shape._sizes[0], None, ckpt, stream)
+    token, _, _, _, dtype = shape._sizes
+    device = _device(q, "q")
+    src, more = _source(shape, qkv, ckpt, device)
+    _run("vmoba_qk_norm_rope" if more else "vmoba_qk_norm_rope_act8", device, shape._ref,
+         _norm(shape, nr, device), *src, _at(q, token, dtype, device, "q"),
+         _at(k, token, dtype, device, "k"), _at(v, token, dtype, device, "v"), *more,
+         _stream(device, stream))
 
 
 def qk_norm_rope_partition(shape, nr, qkv, q, k_perm, v_perm, blocks, ckpt=None,
@@ -235,10 +232,13 @@ def qk_norm_rope_partition(shape, nr, qkv, q, k_perm, v_perm, blocks, ckpt=None,
     """As qk_norm_rope, into the sparse layer's buffers (in place of
     partition): q in token order, k_perm, v_perm in partition order and the
     fp32 means ``blocks`` of the rotated keys (before rounding to storage)."""
-    if blocks is None:
-        raise ValueError("blocks: expected a tensor")
-    _forward("vmoba_qk_norm_rope_partition", shape, nr, qkv, q, k_perm, v_perm, shape._sizes[1],
-             blocks, ckpt, stream)
+    token, head, _, means, dtype = shape._sizes
+    device = _device(q, "q")
+    src, more = _source(shape, qkv, ckpt, device)
+    _run("vmoba_qk_norm_rope_partition" if more else "vmoba_qk_norm_rope_partition_act8", device,
+         shape._ref, _norm(shape, nr, device), *src, _at(q, token, dtype, device, "q"),
+         _at(k_perm, head, dtype, device, "k_perm"), _at(v_perm, head, dtype, device, "v_perm"),
+         _at(blocks, means, _F32, device, "blocks"), *more, _stream(device, stream))
 
 
 def qk_norm_rope_bwd_workspace_size(shape: LayerShape) -> int:
@@ -262,10 +262,11 @@ def qk_norm_rope_bwd(shape, nr, qkv, dq, dk, dv, dqkv, dweight, ws, stream=None)
     dw = p_ws = n_ws = 0
     if dweight is not None:
         dw = _at(dweight, (2, token[2]), _F32, device, "dweight")
-        p_ws, n_ws = _at(ws, ws.shape, ws.dtype, device, "ws"), ws.numel() * ws.element_size()
-    _run(name, device, stream, shape._ref, _norm(shape, nr, device), *src,
+        p_ws, n_ws = _at(ws, ws.shape, ws.dtype, device, "ws"), ws.nbytes
+    _run(name, device, shape._ref, _norm(shape, nr, device), *src,
          _at(dq, token, dtype, device, "dq"), _at(dk, token, dtype, device, "dk"),
-         _at(dv, token, dtype, device, "dv"), *_raw(shape, dqkv, device, "dqkv"), dw, p_ws, n_ws)
+         _at(dv, token, dtype, device, "dv"), *_raw(shape, dqkv, device, "dqkv"), dw, p_ws, n_ws,
+         _stream(device, stream))
 
 
 def _rows(x, name):
@@ -295,8 +296,8 @@ def act8_pack(x, ckpt, stream=None) -> None:
     code, rows, cols, ld = _rows(x, "x")
     device = _device(x, "x")
     codes, scales = _ckpt(ckpt, x.shape, ckpt.group, device, "ckpt")
-    _run("vmoba_act8_pack", device, stream, code, x.data_ptr(), rows, cols, ld, ckpt.group, codes,
-         scales)
+    _run("vmoba_act8_pack", device, code, x.data_ptr(), rows, cols, ld, ckpt.group, codes, scales,
+         _stream(device, stream))
 
 
 def act8_unpack(ckpt, out, stream=None) -> None:
@@ -305,5 +306,5 @@ def act8_unpack(ckpt, out, stream=None) -> None:
     code, rows, cols, ld = _rows(out, "out")
     device = _device(out, "out")
     codes, scales = _ckpt(ckpt, out.shape, ckpt.group, device, "ckpt")
-    _run("vmoba_act8_unpack", device, stream, code, codes, scales, rows, cols, ckpt.group,
-         out.data_ptr(), ld)
+    _run("vmoba_act8_unpack", device, code, codes, scales, rows, cols, ckpt.group, out.data_ptr(),
+         ld, _stream(device, stream))

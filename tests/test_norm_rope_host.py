@@ -146,8 +146,9 @@ def test_binding_refuses_before_the_call():
             ("one tensor or three", lambda: V.qk_norm_rope(sh, nr, (t, t), t, t, t)),
             ("k: expected a contiguous",
              lambda: V.qk_norm_rope(sh, nr, _Fake(qkv), t, _Fake(qkv[:, 0]), t)),
-            ("blocks: expected a tensor",
-             lambda: V.qk_norm_rope_partition(sh, nr, _Fake(qkv), t, t, t, None))):
+            ("blocks: expected shape",
+             lambda: V.qk_norm_rope_partition(sh, nr, _Fake(qkv), t, _Fake(host.view(h, s, d)),
+                                              _Fake(host.view(h, s, d)), t))):
         with pytest.raises(ValueError, match=match):
             call()
     with pytest.raises(ValueError, match="checkpoint"):
