@@ -199,7 +199,9 @@ class VMoBASelfAttention(torch.nn.Module):
         self.layer = VMoBALayer(self.shape, device=device)
         self.scale = 1.0 / math.sqrt(self.head_dim)
         self.norm_eps, self.checkpoint8 = float(norm_eps), bool(checkpoint8)
-        self.rope_dims = (0, 0, 0)
+        # like the layer's buffers, the rotation's table is the module's own: fp32
+        # whatever type the parameters are moved to
+        self.rope_dims, self.rope_table = (0, 0, 0), None
         self.q_norm = self.k_norm = None
         if qk_norm:
             self.q_norm, self.k_norm = (
@@ -207,8 +209,8 @@ class VMoBASelfAttention(torch.nn.Module):
                 for _ in range(2))
         if rope:
             self.rope_dims = norm_rope.rope_dims(self.head_dim) if rope is True else tuple(rope)
-            self.register_buffer("rope_table", norm_rope.rope_table(
-                self.shape, self.rope_dims, rope_base, rope_origin, device), persistent=False)
+            self.rope_table = norm_rope.rope_table(self.shape, self.rope_dims, rope_base,
+                                                   rope_origin, device)
 
     def forward(self, x: torch.Tensor, full_attention: bool = False) -> torch.Tensor:
         s = x.shape[0]
@@ -217,9 +219,9 @@ class VMoBASelfAttention(torch.nn.Module):
             linear = Linear8Function.apply if keep8 else torch.nn.functional.linear
             qkv = linear(x, self.qkv.weight, self.qkv.bias)
             o = VMoBANormRopeFunction.apply(
-                qkv.view(s, 3, self.n_heads, self.head_dim), self.q_norm, self.k_norm, self.layer,
-                getattr(self, "rope_table", None), self.rope_dims, self.norm_eps, self.tau,
-                bool(full_attention), self.scale, keep8)
+                qkv.view(s, 3, self.n_heads, self.head_dim), self.q_norm.float(),
+                self.k_norm.float(), self.layer, self.rope_table, self.rope_dims, self.norm_eps,
+                self.tau, bool(full_attention), self.scale, keep8)
             return linear(o.view(s, -1), self.proj.weight, self.proj.bias)
         qkv = self.qkv(x).view(s, 3, self.n_heads, self.head_dim)
         q, k, v = (qkv[:, i].contiguous() for i in range(3))

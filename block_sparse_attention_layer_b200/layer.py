@@ -45,8 +45,9 @@ class VMoBALayer:
         self.dq = torch.empty((s, h, d), dtype=dt, device=dev)
         self.dk = torch.empty((s, h, d), dtype=dt, device=dev)
         self.dv = torch.empty((s, h, d), dtype=dt, device=dev)
-        # forwards run so far: lets a caller tell whether the forward state in
-        # the buffers (LSE, fp32 output copy, pair lists) is still its own
+        # forwards (and prologues) run so far: lets a caller tell whether the
+        # forward state in the buffers (LSE, fp32 output copy, pair lists) is
+        # still its own
         self.generation = 0
         self._device = dev
 
@@ -68,7 +69,9 @@ class VMoBALayer:
         """Raw rows of the projection (or their Act8 checkpoint) -> self.q,
         self.k_perm, self.v_perm and self.blocks: norm, rotation, partition
         and pooling in one pass (norm_rope.qk_norm_rope_partition); ckpt: an
-        Act8 to store the raw rows in."""
+        Act8 to store the raw rows in.  The state of an earlier forward ends
+        here (as a forward does, this counts as a new generation)."""
+        self.generation += 1
         norm_rope.qk_norm_rope_partition(self.shape, norm, qkv, self.q, self.k_perm, self.v_perm,
                                          self.blocks, ckpt=ckpt)
 

@@ -137,3 +137,22 @@ def test_side_stream_and_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, _roundtrip(x, 128)[1])
+
+
+def test_offsets_beyond_32_bits():
+    """More than 2^32 values: the last rows are those of a call on them alone."""
+    rows, cols = 2 ** 22 + 3, 1032
+    x = torch.empty((rows, cols), dtype=torch.bfloat16, device="cuda")
+    part = torch.randn((2 ** 16, cols), device="cuda").to(torch.bfloat16)
+    for i in range(0, rows, 2 ** 16):
+        x[i:i + 2 ** 16] = (part * (1 + i))[:rows - i]
+    ckpt = V.Act8.empty((rows, cols), 128)
+    V.act8_pack(x, ckpt)
+    tail = V.Act8.empty((1000, cols), 128)
+    V.act8_pack(x[-1000:], tail)
+    assert torch.equal(ckpt.codes[-1000:], tail.codes)
+    assert torch.equal(ckpt.scales[-1000:], tail.scales)
+    out = torch.empty((1000, cols), dtype=x.dtype, device="cuda")
+    V.act8_unpack(tail, out)
+    V.act8_unpack(ckpt, x)
+    assert torch.equal(x[-1000:], out)

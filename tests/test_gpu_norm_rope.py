@@ -372,6 +372,47 @@ def test_full_size_sampled():
     assert np.array_equal(ckpt.scales[:, 1].cpu().numpy(), scales)
 
 
+def test_offsets_beyond_32_bits():
+    """Raw rows, outputs and checkpoint of more than 2^32 bytes: the last and
+    middle blocks equal those of a small run on the same rows."""
+    grid, h, d = (64, 64, 64), 24, 128
+    dims = (0, 0, 0)
+    sh = V.LayerShape(*grid, h, d, 0, 4, 64, 64, "bf16")
+    s = sh.s
+    qkv = torch.empty((s, 3, h, d), dtype=torch.bfloat16, device="cuda")
+    assert qkv.nbytes > 2 ** 32
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    part = torch.randn((4096, 3, h, d), generator=gen, device="cuda").to(torch.bfloat16)
+    for i in range(s // 4096):
+        qkv[i * 4096:(i + 1) * 4096] = part * (1 + i)
+    nr = V.NormRope(dims=dims)
+    q = torch.empty((s, h, d), dtype=torch.bfloat16, device="cuda")
+    k, v = torch.empty((h, s, d), dtype=q.dtype, device="cuda"), torch.empty((h, s, d), dtype=q.dtype,
+                                                                             device="cuda")
+    blocks = torch.empty((h, 16, d), device="cuda")
+    ckpt = V.Act8.empty((s, 3, h, d), d)
+    V.qk_norm_rope_partition(sh, nr, qkv, q, k, v, blocks, ckpt=ckpt)
+    dqkv = torch.empty_like(qkv)
+    V.qk_norm_rope_bwd(sh, nr, qkv, q, q, q, dqkv, None, None)
+    small = V.LayerShape(4, 64, 64, h, d, 0, 4, 64, 64, "bf16")
+    n = small.s
+    for j in (0, 7, 15):
+        rows = slice(j * n, (j + 1) * n)
+        out = [torch.empty_like(q[:n]), torch.empty((h, n, d), dtype=q.dtype, device="cuda"),
+               torch.empty((h, n, d), dtype=q.dtype, device="cuda"),
+               torch.empty((h, 1, d), device="cuda")]
+        c = V.Act8.empty((n, 3, h, d), d)
+        V.qk_norm_rope_partition(small, nr, qkv[rows], *out, ckpt=c)
+        assert torch.equal(q[rows], out[0]) and torch.equal(k[:, rows], out[1])
+        assert torch.equal(v[:, rows], out[2]) and torch.equal(ckpt.codes[rows], c.codes)
+        assert torch.equal(ckpt.scales[rows], c.scales)
+        # fp32 sums of at most 64 rows a lane, cut differently
+        assert (blocks[:, j] - out[3][:, 0]).abs().max() <= 2 * 64 * R.U * out[1].abs().max()
+        back = torch.empty_like(qkv[rows])
+        V.qk_norm_rope_bwd(small, nr, qkv[rows], q[rows], q[rows], q[rows], back, None, None)
+        assert torch.equal(dqkv[rows], back)
+
+
 def test_refusals_leave_outputs_alone():
     c = Case((2, 4, 4), 2, 64, "bf16", seed=13)
     out = [c.token(), c.head(), c.head(), c.means()]

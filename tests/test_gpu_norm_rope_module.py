@@ -158,6 +158,19 @@ def test_shared_layer_rebuilds(ckpt):
         assert torch.equal(gq.grad, dw[0]) and torch.equal(gk.grad, dw[1])
 
 
+def test_prologue_without_a_forward_ends_the_state():
+    """A prologue on the same layer between forward and backward (nothing else)
+    overwrites keys and queries: the backward must rebuild, not use them."""
+    table, layer = _table(), _layer()
+    qkv, gq, gk, dout = _inputs(45)
+    out = _apply(layer, qkv, gq, gk, table)
+    other = _inputs(46, leaf=False)
+    layer.prologue(other[0], V.NormRope(other[1], other[2], EPS, table, DIMS))
+    out.backward(dout)
+    _, dqkv, dw = _by_hand(_layer(), qkv.detach(), gq.detach(), gk.detach(), dout, table)
+    assert torch.equal(qkv.grad, dqkv) and torch.equal(gq.grad, dw[0])
+
+
 def test_weights_may_be_absent_or_frozen():
     table = _table()
     qkv, gq, gk, dout = _inputs(50)
@@ -203,7 +216,7 @@ def _module(ckpt, **kw):
 
 def _saved_bytes(m, x):
     """What autograd holds for the backward, without parameters and tables."""
-    kept = {id(p) for p in m.parameters()} | {id(b) for b in m.buffers()}
+    kept = {id(p) for p in m.parameters()} | {id(m.rope_table)}
     size = []
     with torch.autograd.graph.saved_tensors_hooks(
             lambda t: (size.append(0 if id(t) in kept or t.dim() < 2 else
@@ -232,6 +245,16 @@ def test_module_trains_with_and_without_checkpoints():
         assert torch.equal(small(x), y0.detach())
         full = small(x, full_attention=True)
     assert full.shape == x.shape and torch.isfinite(full).all()
+
+
+def test_module_moved_to_another_type():
+    """Norm weights moved to bf16 with the rest: used and trained in fp32."""
+    x = (torch.randn((S, NH * D), device="cuda") * 0.5).to(torch.bfloat16)
+    m, moved = _module(False), _module(False).to(torch.bfloat16)
+    assert moved.q_norm.dtype == torch.bfloat16 and moved.rope_table.dtype == torch.float32
+    assert torch.equal(m(x), moved(x))
+    moved(x).float().square().mean().backward()
+    assert moved.q_norm.grad.dtype == torch.bfloat16 and torch.isfinite(moved.q_norm.grad).all()
 
 
 def test_module_arguments():
