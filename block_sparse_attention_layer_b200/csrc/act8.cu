@@ -1,8 +1,10 @@
 // Activation checkpoints in 8 bits: [rows][cols] values as int8 codes and one
 // fp32 scale for each group of `group` neighbouring columns (the last group of
-// a row may be short), and back.  Arithmetic of a group: rows.cuh.  Both passes
-// are HBM bound: one read of the values, one write of 1 + 4 / group bytes for
-// each, or the reverse.
+// a row may be short), and back.  Arithmetic of a group: rows.cuh.  Bound: HBM,
+// one read of the values and one write of 1 + 4 / group bytes for each, or the
+// reverse.  55296 x 1536 bf16 in groups of 128: 49 us to store (5.2 TB/s, 0.81
+// of a plain copy's rate; half of its instructions are integer ones, for the
+// codes), 40 us to read back (0.99).
 //
 // A group lies over group / 8 lanes, eight values a lane: neighbouring columns
 // in 16-byte accesses where every row starts on a 16-byte boundary and its
@@ -39,7 +41,8 @@ __device__ __forceinline__ void store8(float* p, const Vals& v) {
 }
 
 // Groups in order of rows.  A CTA takes kUnroll * kThreads / G of them in a
-// row; the 64-bit division that finds the first one's row is the CTA's, a
+// row, a lane kUnroll with all their loads in flight (store and read back with
+// two: 97 us, four: 94, eight: 104); the 64-bit division that finds the first one's row is the CTA's, a
 // lane finds its own from there by a 32-bit multiplication.
 constexpr int kUnroll = 4;
 

@@ -5,16 +5,24 @@
 // layer's partition order together with the fp32 block means of k, so that
 // the sparse layer needs no partition pass over them.  The raw rows come from
 // the projection or from an 8-bit checkpoint, and the pass can write that
-// checkpoint.  A row's raw value is read once and its result written once:
-// HBM bound, 6 s n_h d elements.
+// checkpoint.
+//
+// Bound: HBM.  Each raw value is read once, each result written once: 6 s n_h d
+// elements (3 of them 1.03 bytes when they come from codes, 3.1 s n_h d bytes
+// more when a checkpoint is written).  55296 tokens, 12 heads of 128, bf16:
+// 162 us into 288 blocks (6.3 TB/s, 0.97 of a plain copy's 6.46), 176 us into
+// eight blocks, 214 us with the checkpoint written (0.93), 137 us from it
+// (0.88).
 //
 // A lane works on two rows of q, k and v at a time, two neighbouring heads of
 // one token where the head count is even (they share the position and its
-// table entries), else one head of two tokens: six loads in flight before the
-// first is used, and the four sums of squares go through one shuffle tree.  A
-// CTA's eight warps take `up` neighbouring units of heads, the rest of the
-// warps further tokens.  A block of keys is cut into chunks, one CTA each;
-// the CTAs of a block are a cluster, whose members add their column sums over
+// table entries), else one head of two tokens; the four sums of squares go
+// through one shuffle tree.  Rows reach a lane through its own place in shared
+// memory by asynchronous copies, two steps ahead: loads in registers at two
+// CTAs an SM left 55296 tokens at 244 us where these took 202.  A CTA's eight
+// warps take `up` neighbouring units of heads, the rest of the warps further
+// tokens.  A block of keys may be cut into chunks, one CTA each; the CTAs of a
+// block are then a cluster, whose members add their column sums over
 // distributed shared memory in a fixed order.  Token order is the case of a
 // single block that is the whole latent, without clusters.
 #include <cooperative_groups.h>
@@ -110,8 +118,8 @@ struct Feed<E, D, true, TwoHeads> {
   }
 };
 
-// Iterations a warp's loads run ahead, and the CTAs of an SM that this leaves
-// shared memory for.
+// Steps of a warp in shared memory: the one at work and those being loaded
+// (as many as leave room for two CTAs an SM, or for fp32 rows one).
 template <typename E, bool From8>
 constexpr int stages() { return From8 || sizeof(E) == 2 ? 3 : 2; }
 

@@ -20,9 +20,6 @@
 #include "common.cuh"
 
 namespace vmoba {
-
-struct NormRopeArgs;
-
 namespace rows {
 
 constexpr unsigned kAll = 0xFFFFFFFFu;
@@ -59,7 +56,7 @@ __device__ __forceinline__ int elem_at(int l, int i) {
   return i < 4 ? l * 4 + i : D / 2 + l * 4 + i - 4;
 }
 
-// Rows pass once: they leave L1 to the rotation table and the weights.
+// Values pass once: no place in L1.
 __device__ __forceinline__ uint4 load16(const void* p) {
   uint4 v;
   asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -237,21 +234,6 @@ __device__ __forceinline__ void spread(float s, float (&v)[4]) {
   for (int k = 0; k < 4; ++k) v[k] = __shfl_sync(kAll, s, k * (G / 4), G);
 }
 
-// The same for two rows; sum k is with lane k * G / 2 of the group.
-template <int G>
-__device__ __forceinline__ float half_sums(const float (&v)[2], int l) {
-  const bool hi = l & (G / 2);
-  float s = (hi ? v[1] : v[0]) + __shfl_xor_sync(kAll, hi ? v[0] : v[1], G / 2);
-#pragma unroll
-  for (int o = G / 4; o > 0; o >>= 1) s += __shfl_xor_sync(kAll, s, o);
-  return s;
-}
-template <int G>
-__device__ __forceinline__ void spread(float s, float (&v)[2]) {
-#pragma unroll
-  for (int k = 0; k < 2; ++k) v[k] = __shfl_sync(kAll, s, k * (G / 2), G);
-}
-
 // Sum over the G lanes of a row.
 template <int G>
 __device__ __forceinline__ float row_sum(float v) {
@@ -348,6 +330,9 @@ __device__ __forceinline__ float max_abs3(float a, float b, float c) {
 // only tie is 63.5 (x = a / 2), which goes up to 64.  A factor 2^-19 larger
 // than 127 / a therefore rounds every quotient as asked (checked for every
 // pair of significands); with 254 / 128 each value is settled exactly.
+// That is one fma a value; testing every quotient's distance from a border
+// instead, as fp32 does, sent half of the groups the settling way (an element
+// is a / 2 in that many) and took 71 us against 55 for 55296 x 1536.
 // fp32: where a quotient's distance from its integer is so close to a half
 // that the factor's error could decide, the lane settles its eight.
 // A group with a outside [2^-119, 2^100] (nothing to scale, not finite, or
@@ -448,28 +433,26 @@ __device__ __forceinline__ float rsqrt_normal(float v) {
   return r;
 }
 
-// r[k] = 1 / sqrt(mean x^2 + eps) of two or four rows.  Where a row's squares
-// leave fp32's range it is first scaled by pre[k] = 2^-80 (x changes; eps then
-// is far below the mean's last bit); else pre[k] = 1.
-template <int D, int N>
-__device__ __forceinline__ void inv_rms(Vals (&x)[N], float eps, int l, float (&r)[N],
-                                        float (&pre)[N]) {
+// r[k] = 1 / sqrt(mean x^2 + eps) of four rows.  Where a row's squares leave
+// fp32's range it is first scaled by pre[k] = 2^-80 (x changes, and eps is
+// taken times its square); else pre[k] = 1.
+template <int D>
+__device__ __forceinline__ void inv_rms(Vals (&x)[4], float eps, int l, float (&r)[4],
+                                        float (&pre)[4]) {
   constexpr int G = D / 8;
-  float ss[N];
+  float ss[4];
 #pragma unroll
-  for (int k = 0; k < N; ++k) {
+  for (int k = 0; k < 4; ++k) {
     ss[k] = lane_dot(x[k], x[k]);
     pre[k] = 1.f;
   }
-  float s;
-  if constexpr (N == 4) s = quarter_sums<G>(ss, l);
-  else s = half_sums<G>(ss, l);
+  const float s = quarter_sums<G>(ss, l);
   spread<G>(rsqrt_normal(fmaf(s, 1.0f / D, eps)), r);
   if (__any_sync(kAll, !(s < 0x1p100f))) {
-    float sum[N];
+    float sum[4];
     spread<G>(s, sum);
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
+    for (int k = 0; k < 4; ++k) {
       const bool big = !(sum[k] < 0x1p100f);
       if (big) {
         pre[k] = 0x1p-80f;
@@ -477,7 +460,7 @@ __device__ __forceinline__ void inv_rms(Vals (&x)[N], float eps, int l, float (&
         for (int i = 0; i < 8; ++i) x[k].at(i) *= 0x1p-80f;
       }
       const float again = row_sum<G>(lane_dot(x[k], x[k]));
-      if (big) r[k] = rsqrt_normal(again * (1.0f / D));
+      if (big) r[k] = rsqrt_normal(fmaf(again, 1.0f / D, eps * 0x1p-80f * 0x1p-80f));
     }
   }
 }
@@ -600,18 +583,6 @@ __device__ __forceinline__ Vals load_weights(const float* g, int l) {
   return w;
 }
 
-// The weights of q and k (2 D) in shared memory: a lane's first four and last
-// four elements lie in separate halves (16-byte reads without bank conflicts).
-template <typename E, int D>
-__device__ __forceinline__ void place_weight(const NormRopeArgs& a, int c, float* to);
-template <int D>
-__device__ __forceinline__ Vals weights(const float* g, int l) {
-  const float4 a = reinterpret_cast<const float4*>(g)[l];
-  const float4 b = reinterpret_cast<const float4*>(g + D / 2)[l];
-  return {make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y),
-          make_float2(b.z, b.w)};
-}
-
 }  // namespace rows
 
 // Launches a kernel that begins with after_previous(): it may be set up while
@@ -663,15 +634,6 @@ struct NormRopeArgs {
   int ht, hh, hw;             // pairs that turn with t, y, x
   bool still;                 // whether some pairs do not turn (the table has nothing for them)
 };
-
-namespace rows {
-template <typename E, int D>
-__device__ __forceinline__ void place_weight(const NormRopeArgs& a, int c, float* to) {
-  const float* g = c < D ? a.gq : a.gk;
-  const int half = c % D / (D / 2), l = c % (D / 2) / 4;
-  to[c] = g ? __ldg(g + elem_at<E, D>(l, half * 4 + c % 4)) : 1.f;
-}
-}  // namespace rows
 
 struct NormRopeOut {
   void *q, *k, *v;

@@ -160,6 +160,7 @@ CASES = {
                              box=(2, 2, 2), weights=False, layout="padded"),
     "long block": dict(grid=(2, 40, 60), h=1, d=64, dtype="bf16", box=(2, 40, 60)),
     "2048 tokens": dict(grid=(8, 16, 16), h=4, d=64, dtype="bf16", box=(2, 4, 4)),
+    "huge rows and eps": dict(grid=(2, 4, 4), h=2, d=64, dtype="f32", eps=1e33, scale=1e16),
     "large eps": dict(grid=(2, 4, 4), h=2, d=64, dtype="f32", eps=10.0),
 }
 
