@@ -81,11 +81,13 @@ class LayerShape:
         return ctypes.byref(self.c())
 
     @functools.cached_property
-    def _sizes(self):
-        """(shapes of token-order rows, partition-order rows, raw rows, block
-        means, torch dtype)."""
-        s, h, d = self.s, self.n_heads, self.head_dim
-        return (s, h, d), (h, s, d), (s, 3, h, d), (h, num_blocks(self), d), _torch_dtype(self)
+    def _native(self):
+        """The shape as norm_rope's calls take it."""
+        from . import norm_rope
+        if not norm_rope._bound:
+            norm_rope._bind()
+        c = self.c()
+        return norm_rope._calls.shape(*(getattr(c, name) for name, _ in c._fields_), num_blocks(self))
 
     def c(self) -> CShape:
         return CShape(self.T, self.H, self.W, self.n_heads, self.head_dim, self.mode,

@@ -5,7 +5,9 @@ Usage: python -m block_sparse_attention_layer_b200.build [--force] [-j N]
 Every .cu file under csrc/ is compiled for sm_100a only
 (-gencode arch=compute_100a,code=sm_100a) with -lineinfo and linked into
 block_sparse_attention_layer_b200/libvmoba.so against the static CUDA
-runtime.  Rebuilds only when a source or header is newer than the library.
+runtime; csrc/calls.cpp, the Python calls of norm_rope.py, is compiled against
+torch's headers into _calls.so beside it.  Rebuilds only when a source or
+header is newer than what was built from it.
 """
 from __future__ import annotations
 
@@ -22,6 +24,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libvmoba.so")
+CALLS = os.path.join(PKG, "_calls.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O3",
@@ -64,7 +67,34 @@ def _compile(src: str, verbose_ptxas: bool) -> str:
     return obj
 
 
+def build_calls(force: bool = False) -> str:
+    """Compile csrc/calls.cpp against the installed torch."""
+    src = os.path.join(CSRC, "calls.cpp")
+    deps = [src, *glob.glob(os.path.join(ROOT, "include", "*.h"))]
+    if not force and os.path.exists(CALLS) and \
+            all(os.path.getmtime(p) <= os.path.getmtime(CALLS) for p in deps):
+        return CALLS
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    include = [sysconfig.get_path("include"), os.path.join(root, "include"),
+               os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    cxx = os.environ.get("CXX") or shutil.which("g++") or "c++"
+    cmd = [cxx, "-O2", "-std=c++17", "-shared", "-fPIC", *("-I" + i for i in include),
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", src,
+           "-o", CALLS + ".tmp", "-L" + os.path.join(root, "lib"),
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cxx} failed for {src}:\n{r.stderr}")
+    os.replace(CALLS + ".tmp", CALLS)
+    return CALLS
+
+
 def build(force: bool = False, jobs: int = 0, verbose_ptxas: bool = False) -> str:
+    build_calls(force)
     if not force and up_to_date():
         return LIB
     os.makedirs(OBJ, exist_ok=True)

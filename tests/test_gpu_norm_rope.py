@@ -428,8 +428,11 @@ def test_refusals_leave_outputs_alone():
         V.qk_norm_rope_bwd(c.sh, c.nr, c.qkv, *c.grads, c.buffer()[1],
                            torch.zeros((2, 64), device="cuda"),
                            torch.zeros(16, dtype=torch.uint8, device="cuda"))
-    with pytest.raises(ValueError, match="CUDA"):
-        V.qk_norm_rope(c.sh, c.nr, c.qkv, *(t.cpu() for t in out[:3]))
+    with pytest.raises(ValueError, match="v: expected a CUDA"):
+        V.qk_norm_rope(c.sh, c.nr, c.qkv, c.token(), c.token(), c.token().cpu())
+    with pytest.raises(ValueError, match="table: expected a CUDA"):
+        V.qk_norm_rope(c.sh, V.NormRope(c.gq, c.gk, EPS, c.table.cpu(), c.dims), c.qkv, c.token(),
+                       c.token(), c.token())
     torch.cuda.synchronize()
     assert V.kernel_launches() == n0
     assert all((t == 9.0).all() for t in out)

@@ -7,7 +7,7 @@ import numpy as np
 import pytest
 
 import block_sparse_attention_layer_b200 as V
-from block_sparse_attention_layer_b200 import _lib, norm_rope
+from block_sparse_attention_layer_b200 import _lib
 
 from . import norm_rope_ref as R
 
@@ -116,95 +116,100 @@ def test_workspace_sizes():
     assert V.qk_norm_rope_bwd_workspace_size(_shape(bt=3)) == 0
 
 
-class _Fake:
-    """A stand-in with a CUDA tensor's attributes: what the layout checks read."""
-
-    def __init__(self, t, device="cuda:0"):
-        self.t, self.device = t, torch.device(device)
-        self.shape, self.dtype, self.is_cuda = t.shape, t.dtype, True
-        self.get_device = lambda: self.device.index
-
-    def __getattr__(self, name):
-        return getattr(self.t, name)
-
-
 def test_binding_refuses_before_the_call():
+    """Everything about a tensor is checked before its device, so host tensors
+    reach each check; a call that is right but for the device is refused last."""
     sh = _shape()
     s, h, d = sh.s, 2, 64
     bf = torch.bfloat16
-    host = torch.zeros((s, h, d), dtype=bf)
-    t, qkv = _Fake(host), torch.zeros((s, 3, h, d), dtype=bf)
-    nr = V.NormRope()
+    t, qkv = torch.zeros((s, h, d), dtype=bf), torch.zeros((s, 3, h, d), dtype=bf)
+    head = t.view(h, s, d)
+    wide = torch.zeros((s, 3 * h * d + 64), dtype=bf)
+    padded = wide.as_strided((s, 3, h, d), (wide.stride(0), h * d, d, 1))
+    nr, table = V.NormRope(), torch.zeros(((4 * 2 + 8 * 4 + 8 * 6) // 2, 2))
+    c, x = V.Act8.empty((s, 3, h, d), d, "cpu"), torch.zeros((4, 8))
+    means, dw = torch.zeros((h, 8, d)), torch.zeros((2, d))
+    ws = torch.zeros(V.qk_norm_rope_bwd_workspace_size(sh), dtype=torch.uint8)
+
+    def fwd(qkv=qkv, q=t, k=t, v=t, nr=nr, **kw):
+        V.qk_norm_rope(sh, nr, qkv, q, k, v, **kw)
+
+    def part(q=t, k=head, v=head, blocks=means):
+        V.qk_norm_rope_partition(sh, nr, qkv, q, k, v, blocks)
+
+    def bwd(qkv=qkv, dq=t, dk=t, dv=t, out=qkv, dweight=dw, ws=ws):
+        V.qk_norm_rope_bwd(sh, nr, qkv, dq, dk, dv, out, dweight, ws)
+
+    def norm(**kw):
+        fwd(nr=V.NormRope(**kw))
+
     for match, call in (
-            ("q: expected a CUDA", lambda: V.qk_norm_rope(sh, nr, qkv, host, t, t)),
-            ("qkv: expected a CUDA", lambda: V.qk_norm_rope(sh, nr, qkv, t, t, t)),
-            ("v: expected a CUDA", lambda: V.qk_norm_rope(sh, nr, _Fake(qkv), t, t, host)),
-            ("k: expected a tensor on cuda:0",
-             lambda: V.qk_norm_rope(sh, nr, _Fake(qkv), t, _Fake(host, "cuda:1"), t)),
-            ("qkv: expected shape", lambda: V.qk_norm_rope(sh, nr, _Fake(qkv[1:]), t, t, t)),
-            ("qkv: expected dtype", lambda: V.qk_norm_rope(sh, nr, _Fake(qkv.float()), t, t, t)),
-            ("one tensor or three", lambda: V.qk_norm_rope(sh, nr, (t, t), t, t, t)),
-            ("k: expected a contiguous",
-             lambda: V.qk_norm_rope(sh, nr, _Fake(qkv), t, _Fake(qkv[:, 0]), t)),
-            ("blocks: expected shape",
-             lambda: V.qk_norm_rope_partition(sh, nr, _Fake(qkv), t, _Fake(host.view(h, s, d)),
-                                              _Fake(host.view(h, s, d)), t))):
+            ("qkv: expected a CUDA", fwd), ("qkv: expected a CUDA", part),
+            ("qkv: expected a CUDA", bwd),
+            ("qkv: expected a CUDA", lambda: fwd(qkv=padded)),
+            ("qkv: expected a CUDA", lambda: fwd(qkv=(t, t, t))),
+            ("qkv: expected a CUDA", lambda: fwd(qkv=[qkv[:, i] for i in range(3)])),
+            ("qkv.codes: expected a CUDA", lambda: fwd(qkv=c)),
+            ("qkv: expected a tensor", lambda: fwd(qkv=3)),
+            ("qkv: expected shape", lambda: fwd(qkv=qkv[1:])),
+            ("qkv: expected dtype torch.bfloat16, got torch.float32",
+             lambda: fwd(qkv=qkv.float())),
+            ("qkv: expected one tensor or three", lambda: fwd(qkv=(t, t))),
+            ("qkv: expected one token stride", lambda: fwd(qkv=(t, t, qkv[:, 2]))),
+            ("qkv: rows overlap", lambda: fwd(qkv=qkv[:1].expand(s, 3, h, d))),
+            ("qkv: expected dense rows",
+             lambda: fwd(qkv=torch.zeros((s, h, 3, d), dtype=bf).transpose(1, 2))),
+            ("qkv: expected dense rows",
+             lambda: fwd(qkv=torch.zeros((s, 3, d, h), dtype=bf).transpose(2, 3))),
+            ("q: expected shape", lambda: fwd(q=t[1:])),
+            ("k: expected a contiguous", lambda: fwd(k=qkv[:, 0])),
+            ("v: expected dtype", lambda: fwd(v=t.float())),
+            ("checkpoint", lambda: fwd(qkv=c, ckpt=c)),
+            ("ckpt: expected an Act8", lambda: fwd(ckpt=t)),
+            ("ckpt.codes: expected shape",
+             lambda: fwd(ckpt=V.Act8.empty((s, 2, h, d), d, "cpu"))),
+            ("ckpt.scales: expected shape",
+             lambda: fwd(ckpt=V.Act8(c.codes, c.scales[1:], d))),
+            ("ckpt.scales: expected dtype", lambda: fwd(ckpt=V.Act8(c.codes, c.scales.int(), d))),
+            ("ckpt.codes: expected a contiguous",
+             lambda: fwd(ckpt=V.Act8(torch.zeros((s, 3, h, 2 * d), dtype=torch.int8)[..., :d],
+                                     c.scales, d))),
+            ("groups of 64, got 128", lambda: fwd(ckpt=V.Act8.empty((s, 3, h, d), 128, "cpu"))),
+            ("k_perm: expected shape", lambda: part(k=t)),
+            ("blocks: expected shape", lambda: part(blocks=means[:, 1:])),
+            ("blocks: expected a tensor", lambda: part(blocks=None)),
+            ("dk: expected shape", lambda: bwd(dk=t[1:])),
+            ("dqkv: rows overlap", lambda: bwd(out=qkv[:1].expand(s, 3, h, d))),
+            ("dweight: expected shape", lambda: bwd(dweight=dw[:1])),
+            ("ws: expected a tensor", lambda: bwd(ws=None)),
+            ("dims", lambda: norm(dims=(1, 2, 2))), ("dims", lambda: norm(dims=(64, 2, 0))),
+            ("dims", lambda: norm(dims=(2, 2))), ("dims", lambda: norm(dims=(2.0, 2, 2))),
+            ("dims", lambda: norm(dims=(1 << 70, 2, 2))), ("dims", lambda: norm(dims=None)),
+            ("dims", lambda: norm(dims=(-2, 2, 2))),
+            ("table: expected a rotation table", lambda: norm(dims=(2, 2, 2))),
+            ("table: expected shape", lambda: norm(dims=(2, 2, 2), table=table)),
+            ("qkv: expected a CUDA", lambda: norm(dims=[2, 4, 6], table=table)),
+            ("q_weight: expected shape", lambda: norm(q_weight=torch.zeros(32))),
+            ("k_weight: expected dtype", lambda: norm(k_weight=torch.zeros(64, dtype=bf))),
+            ("64 or 128", lambda: V.Act8.empty((4, 4), 32, "cpu")),
+            ("bfloat16 or float32",
+             lambda: V.act8_pack(x.half(), V.Act8.empty((4, 8), 64, "cpu"))),
+            ("two axes", lambda: V.act8_pack(torch.zeros(4), V.Act8.empty((4,), 64, "cpu"))),
+            ("dense rows", lambda: V.act8_pack(x.t(), V.Act8.empty((8, 4), 64, "cpu"))),
+            ("dense rows",
+             lambda: V.act8_unpack(V.Act8.empty((4, 8), 64, "cpu"), x[:1].expand(4, 8))),
+            ("groups of 64 or 128", lambda: V.act8_pack(x, V.Act8(c.codes, c.scales, 32))),
+            ("ckpt.codes: expected shape",
+             lambda: V.act8_pack(x, V.Act8.empty((4, 9), 64, "cpu"))),
+            ("x: expected a CUDA", lambda: V.act8_pack(x, V.Act8.empty((4, 8), 64, "cpu"))),
+            ("dims", lambda: V.rope_table(sh, (2, 3, 4))),
+            ("CUDA", lambda: V.rope_table(sh, (2, 4, 4), device="cpu"))):
         with pytest.raises(ValueError, match=match):
             call()
-    with pytest.raises(ValueError, match="checkpoint"):
-        c = V.Act8.empty((s, 3, h, d), d, "cpu")
-        V.qk_norm_rope(sh, nr, c, t, t, t, ckpt=c)
-    with pytest.raises(ValueError, match="groups of 64"):
-        V.qk_norm_rope(sh, nr, V.Act8.empty((s, 3, h, d), 128, "cpu"), t, t, t)
-    with pytest.raises(ValueError, match="64 or 128"):
-        V.Act8.empty((4, 4), 32, "cpu")
-    with pytest.raises(ValueError, match="bfloat16 or float32"):
-        V.act8_pack(torch.zeros((4, 4), dtype=torch.float16), V.Act8.empty((4, 4), 64, "cpu"))
-    with pytest.raises(ValueError, match="two axes"):
-        V.act8_pack(torch.zeros(4), V.Act8.empty((4,), 64, "cpu"))
-    with pytest.raises(ValueError, match="dense rows"):
-        V.act8_pack(torch.zeros((4, 8)).t(), V.Act8.empty((8, 4), 64, "cpu"))
-    with pytest.raises(ValueError, match="dense rows"):
-        V.act8_unpack(V.Act8.empty((4, 8), 64, "cpu"), torch.zeros((1, 8)).expand(4, 8))
-    with pytest.raises(ValueError, match="CUDA"):
-        V.act8_pack(torch.zeros((4, 8)), V.Act8.empty((4, 8), 64, "cpu"))
-
-
-def test_raw_rows_layouts():
-    sh = _shape()
-    s, h, d = sh.s, 2, 64
-    bf = torch.bfloat16
-
-    def raw(x):
-        return norm_rope._raw(sh, x, 0, "qkv")
-
-    base = torch.zeros((s, 3 * h * d + 64), dtype=bf)
-    x = base.as_strided((s, 3, h, d), (base.stride(0), h * d, d, 1))
-    *at, ld = raw(_Fake(x))
-    assert ld == 3 * h * d + 64 and [a - at[0] for a in at] == [0, 2 * h * d, 4 * h * d]
-    three = [torch.zeros((s, h, d), dtype=bf) for _ in range(3)]
-    *at, ld = raw([_Fake(t) for t in three])
-    assert ld == h * d and at == [t.data_ptr() for t in three]
-    packed = torch.zeros((s, 3, h, d), dtype=bf)
-    *at, ld = raw([_Fake(packed[:, i]) for i in range(3)])
-    assert ld == 3 * h * d
-    with pytest.raises(ValueError, match="one token stride"):
-        raw([_Fake(three[0]), _Fake(three[1]), _Fake(packed[:, 2])])
-    with pytest.raises(ValueError, match="overlap"):
-        raw(_Fake(packed[:1].expand(s, 3, h, d)))
-    with pytest.raises(ValueError, match="dense rows"):
-        raw(_Fake(torch.zeros((s, h, 3, d), dtype=bf).transpose(1, 2)))
-    with pytest.raises(ValueError, match="cuda:0"):
-        raw([_Fake(three[0]), _Fake(three[1], "cuda:1"), _Fake(three[2])])
-
-
-@pytest.mark.parametrize("kw,match", [
-    (dict(dims=(1, 2, 2)), "even"), (dict(dims=(64, 2, 0)), "even"), (dict(dims=(2, 2)), "even"),
-    (dict(dims=(2, 2, 2)), "rotation table"),
-    (dict(q_weight=torch.zeros(32)), "q_weight"), (dict(k_weight=torch.zeros(64)), "CUDA")])
-def test_norm_arguments_refused(kw, match):
-    with pytest.raises(ValueError, match=match):
-        norm_rope._norm(_shape(), V.NormRope(**kw), 0)
+    with pytest.raises(AttributeError):
+        V.qk_norm_rope(sh, None, qkv, t, t, t)
+    with pytest.raises(V.VmobaError, match="SHAPE"):
+        V.qk_norm_rope(_shape(bt=3), nr, qkv, t, t, t)
 
 
 def test_rope_dims():
