@@ -502,7 +502,8 @@ int vmoba_act8_pack(int dtype, const void* x, long long rows, int cols, long lon
   const int rc = check_act8(dtype, x, rows, cols, ld, group, codes, scales, &none);
   if (rc != VMOBA_OK || none) return rc;
   drop_stale_error();
-  return cuda_status(launch_act8_pack(dtype, x, rows, cols, ld, group, codes, scales, stream));
+  return cuda_status(launch_act8_pack(dtype, x, rows, cols, ld, group, codes, scales, num_sms(),
+                                      stream));
 }
 
 int vmoba_act8_unpack(int dtype, const int8_t* codes, const float* scales, long long rows,
@@ -511,7 +512,8 @@ int vmoba_act8_unpack(int dtype, const int8_t* codes, const float* scales, long 
   const int rc = check_act8(dtype, out, rows, cols, ld, group, codes, scales, &none);
   if (rc != VMOBA_OK || none) return rc;
   drop_stale_error();
-  return cuda_status(launch_act8_unpack(dtype, codes, scales, rows, cols, group, out, ld, stream));
+  return cuda_status(launch_act8_unpack(dtype, codes, scales, rows, cols, group, out, ld,
+                                        num_sms(), stream));
 }
 
 int vmoba_get_status(void* ws, int* device_status, cudaStream_t stream) {

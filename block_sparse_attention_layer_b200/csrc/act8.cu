@@ -40,11 +40,16 @@ __device__ __forceinline__ void store8(float* p, const Vals& v) {
   reinterpret_cast<float4*>(p)[1] = r.b;
 }
 
-// Groups in order of rows.  A CTA takes kUnroll * kThreads / G of them in a
-// row, a lane kUnroll with all their loads in flight (store and read back with
-// two: 97 us, four: 94, eight: 104); the 64-bit division that finds the first one's row is the CTA's, a
-// lane finds its own from there by a 32-bit multiplication.
+// Groups in order of rows.  A CTA takes U * kThreads / G of them in a row, a
+// lane U with all their loads in flight.  U is kUnroll with vectors (store and
+// read back 55296 x 1536 with two: 97 us, four: 94, eight: 104), but one where
+// that makes no more than kFewCtas CTAs an SM (16 x 1536: 2.5 us against 3.1;
+// 1200 x 1536: 4.4 against 4.5; 3000 x 1536: 7.4 against 6.9), and one for
+// single values, eight loads each (40000 x 1003 fp32: 83 us against 115).  The
+// 64-bit division that finds a CTA's first row is done once for it, a lane
+// finds its own from there by a 32-bit multiplication.
 constexpr int kUnroll = 4;
+constexpr int kFewCtas = 6;
 
 struct Shape {
   long long n_groups, ld;
@@ -61,21 +66,21 @@ __device__ __forceinline__ Place place(const Shape& s, long long row0, int g0, i
   return {row0 + down, g - down * s.per_row};
 }
 
-template <typename E, int Group, bool Vec>
+template <typename E, int Group, bool Vec, int U>
 __global__ void __launch_bounds__(kThreads)
 k_act8_pack(const E* __restrict__ x, const __grid_constant__ Shape s, int8_t* __restrict__ codes,
             float* __restrict__ scales) {
   constexpr int G = Group / 8, kPer = kThreads / G;
   const int l = threadIdx.x % G;
-  const long long base = (long long)blockIdx.x * (kUnroll * kPer);
+  const long long base = (long long)blockIdx.x * (U * kPer);
   const long long row0 = base / s.per_row;
   const int g0 = (int)(base - row0 * s.per_row);
-  const int most = (int)min(s.n_groups - base, (long long)(kUnroll * kPer));
-  Raw<E> r[kUnroll];
-  Place at[kUnroll];
+  const int most = (int)min(s.n_groups - base, (long long)(U * kPer));
+  Raw<E> r[U];
+  Place at[U];
   after_previous();
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
+  for (int u = 0; u < U; ++u) {
     const int k = u * kPer + threadIdx.x / G;
     at[u] = place(s, row0, g0, min(k, most - 1));
     at[u].c0 *= Group;
@@ -96,11 +101,11 @@ k_act8_pack(const E* __restrict__ x, const __grid_constant__ Shape s, int8_t* __
     }
   }
 #pragma unroll
-  for (int u = 0; u < kUnroll; u += 2) {
+  for (int u = 0; u < U; u += 2) {
     uint32_t m[2];
-    group_max<G>(r[u], r[u + 1], m[0], m[1]);
+    group_max<G>(r[u], r[min(u + 1, U - 1)], m[0], m[1]);
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < min(2, U); ++b) {
       const int k = (u + b) * kPer + threadIdx.x / G;
       if (k >= most) continue;
       float scale;
@@ -121,22 +126,22 @@ k_act8_pack(const E* __restrict__ x, const __grid_constant__ Shape s, int8_t* __
   }
 }
 
-template <typename E, int Group, bool Vec>
+template <typename E, int Group, bool Vec, int U>
 __global__ void __launch_bounds__(kThreads)
 k_act8_unpack(const int8_t* __restrict__ codes, const float* __restrict__ scales,
               const __grid_constant__ Shape s, E* __restrict__ out) {
   constexpr int G = Group / 8, kPer = kThreads / G;
   const int l = threadIdx.x % G;
-  const long long base = (long long)blockIdx.x * (kUnroll * kPer);
+  const long long base = (long long)blockIdx.x * (U * kPer);
   const long long row0 = base / s.per_row;
   const int g0 = (int)(base - row0 * s.per_row);
-  const int most = (int)min(s.n_groups - base, (long long)(kUnroll * kPer));
-  uint2 w[kUnroll];
-  float scale[kUnroll];
-  Place at[kUnroll];
+  const int most = (int)min(s.n_groups - base, (long long)(U * kPer));
+  uint2 w[U];
+  float scale[U];
+  Place at[U];
   after_previous();
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
+  for (int u = 0; u < U; ++u) {
     const int k = min(u * kPer + (int)threadIdx.x / G, most - 1);
     at[u] = place(s, row0, g0, k);
     at[u].c0 *= Group;
@@ -157,7 +162,7 @@ k_act8_unpack(const int8_t* __restrict__ codes, const float* __restrict__ scales
     }
   }
 #pragma unroll
-  for (int u = 0; u < kUnroll; ++u) {
+  for (int u = 0; u < U; ++u) {
     if (u * kPer + (int)threadIdx.x / G >= most) break;
     const Vals v = decode8(w[u], scale[u]);
     E* dst = out + at[u].row * s.ld;
@@ -174,69 +179,78 @@ k_act8_unpack(const int8_t* __restrict__ codes, const float* __restrict__ scales
   }
 }
 
-template <int Group>
-Shape shape_of(long long n_rows, int cols, long long ld, unsigned* ctas) {
+bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// Calls f(shape, CTAs, vectors?, groups a lane) with compile-time flags.
+template <typename E, int Group, typename F>
+cudaError_t with_shape(const void* x, long long n_rows, int cols, long long ld,
+                       const int8_t* codes, int num_sms, F f) {
   Shape s{};
   s.per_row = (cols + Group - 1) / Group;
   s.cols = cols;
   s.ld = ld;
   s.n_groups = n_rows * s.per_row;
   s.div = FastDiv(s.per_row);
-  constexpr int per_cta = kUnroll * kThreads / (Group / 8);
-  *ctas = (unsigned)((s.n_groups + per_cta - 1) / per_cta);
-  return s;
-}
-
-bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-
-template <typename E>
-bool vectors(const void* x, long long ld, int cols, const int8_t* codes) {
-  return aligned(x, 16) && (ld * sizeof(E)) % 16 == 0 && cols % 8 == 0 && aligned(codes, 8);
+  constexpr int per = kThreads / (Group / 8);          // groups of a CTA, one a lane
+  const bool vec = aligned(x, 16) && (ld * sizeof(E)) % 16 == 0 && cols % 8 == 0 &&
+                   aligned(codes, 8);
+  const bool few = s.n_groups <= (long long)per * kFewCtas * num_sms;
+  const auto go = [&](auto v, auto u) {
+    constexpr int U = decltype(u)::value;
+    return f(s, dim3((unsigned)((s.n_groups + U * per - 1) / (U * per))), v, u);
+  };
+  using Yes = std::true_type;
+  using No = std::false_type;
+  using One = std::integral_constant<int, 1>;
+  using Many = std::integral_constant<int, kUnroll>;
+  if (!vec) return go(No{}, One{});
+  return few ? go(Yes{}, One{}) : go(Yes{}, Many{});
 }
 
 template <typename E, int Group>
 cudaError_t pack_t(const void* x, long long n_rows, int cols, long long ld, int8_t* codes,
-                   float* scales, cudaStream_t st) {
-  unsigned ctas;
-  const Shape s = shape_of<Group>(n_rows, cols, ld, &ctas);
-  const auto kernel = vectors<E>(x, ld, cols, codes) ? k_act8_pack<E, Group, true>
-                                                     : k_act8_pack<E, Group, false>;
+                   float* scales, int num_sms, cudaStream_t st) {
   VMOBA_TRACE("k_act8_pack", st);
-  return launch(kernel, dim3(ctas), kThreads, 0, 1, st, static_cast<const E*>(x), s, codes, scales);
+  return with_shape<E, Group>(x, n_rows, cols, ld, codes, num_sms,
+                              [&](const Shape& s, dim3 ctas, auto v, auto u) {
+    return launch(k_act8_pack<E, Group, decltype(v)::value, decltype(u)::value>, ctas, kThreads, 0,
+                  1, st, static_cast<const E*>(x), s, codes, scales);
+  });
 }
 
 template <typename E, int Group>
 cudaError_t unpack_t(const int8_t* codes, const float* scales, long long n_rows, int cols,
-                     void* out, long long ld, cudaStream_t st) {
-  unsigned ctas;
-  const Shape s = shape_of<Group>(n_rows, cols, ld, &ctas);
-  const auto kernel = vectors<E>(out, ld, cols, codes) ? k_act8_unpack<E, Group, true>
-                                                       : k_act8_unpack<E, Group, false>;
+                     void* out, long long ld, int num_sms, cudaStream_t st) {
   VMOBA_TRACE("k_act8_unpack", st);
-  return launch(kernel, dim3(ctas), kThreads, 0, 1, st, codes, scales, s, static_cast<E*>(out));
+  return with_shape<E, Group>(out, n_rows, cols, ld, codes, num_sms,
+                              [&](const Shape& s, dim3 ctas, auto v, auto u) {
+    return launch(k_act8_unpack<E, Group, decltype(v)::value, decltype(u)::value>, ctas, kThreads,
+                  0, 1, st, codes, scales, s, static_cast<E*>(out));
+  });
 }
 
 }  // namespace
 
 cudaError_t launch_act8_pack(int dtype, const void* x, long long n_rows, int cols, long long ld,
-                             int group, int8_t* codes, float* scales, cudaStream_t st) {
+                             int group, int8_t* codes, float* scales, int num_sms,
+                             cudaStream_t st) {
   if (dtype == VMOBA_BF16)
     return group == 64
-               ? pack_t<__nv_bfloat16, 64>(x, n_rows, cols, ld, codes, scales, st)
-               : pack_t<__nv_bfloat16, 128>(x, n_rows, cols, ld, codes, scales, st);
-  return group == 64 ? pack_t<float, 64>(x, n_rows, cols, ld, codes, scales, st)
-                     : pack_t<float, 128>(x, n_rows, cols, ld, codes, scales, st);
+               ? pack_t<__nv_bfloat16, 64>(x, n_rows, cols, ld, codes, scales, num_sms, st)
+               : pack_t<__nv_bfloat16, 128>(x, n_rows, cols, ld, codes, scales, num_sms, st);
+  return group == 64 ? pack_t<float, 64>(x, n_rows, cols, ld, codes, scales, num_sms, st)
+                     : pack_t<float, 128>(x, n_rows, cols, ld, codes, scales, num_sms, st);
 }
 
 cudaError_t launch_act8_unpack(int dtype, const int8_t* codes, const float* scales,
                                long long n_rows, int cols, int group, void* out, long long ld,
-                               cudaStream_t st) {
+                               int num_sms, cudaStream_t st) {
   if (dtype == VMOBA_BF16)
     return group == 64
-               ? unpack_t<__nv_bfloat16, 64>(codes, scales, n_rows, cols, out, ld, st)
-               : unpack_t<__nv_bfloat16, 128>(codes, scales, n_rows, cols, out, ld, st);
-  return group == 64 ? unpack_t<float, 64>(codes, scales, n_rows, cols, out, ld, st)
-                     : unpack_t<float, 128>(codes, scales, n_rows, cols, out, ld, st);
+               ? unpack_t<__nv_bfloat16, 64>(codes, scales, n_rows, cols, out, ld, num_sms, st)
+               : unpack_t<__nv_bfloat16, 128>(codes, scales, n_rows, cols, out, ld, num_sms, st);
+  return group == 64 ? unpack_t<float, 64>(codes, scales, n_rows, cols, out, ld, num_sms, st)
+                     : unpack_t<float, 128>(codes, scales, n_rows, cols, out, ld, num_sms, st);
 }
 
 }  // namespace vmoba

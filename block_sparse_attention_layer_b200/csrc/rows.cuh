@@ -652,9 +652,10 @@ cudaError_t launch_norm_rope_bwd(const Prob& P, const NormRopeArgs& a, const voi
 cudaError_t launch_rope_table(int T, int H, int W, int ht, int hh, int hw, double base,
                               const long long (&origin)[3], float2* table, cudaStream_t st);
 cudaError_t launch_act8_pack(int dtype, const void* x, long long n_rows, int cols, long long ld,
-                             int group, int8_t* codes, float* scales, cudaStream_t st);
+                             int group, int8_t* codes, float* scales, int num_sms,
+                             cudaStream_t st);
 cudaError_t launch_act8_unpack(int dtype, const int8_t* codes, const float* scales,
                                long long n_rows, int cols, int group, void* out, long long ld,
-                               cudaStream_t st);
+                               int num_sms, cudaStream_t st);
 
 }  // namespace vmoba
