@@ -8,6 +8,7 @@ library is missing or fails to load, every call raises.
 from __future__ import annotations
 
 import ctypes
+import dataclasses
 import functools
 import math
 import os
@@ -74,7 +75,11 @@ class LayerShape:
     def s(self) -> int:
         return self.T * self.H * self.W
 
-    # what calls on this shape need each time, built once (the fields are frozen)
+    # what calls on this shape need each time, built once (the fields are
+    # frozen); a copied or pickled shape builds its own
+
+    def __getstate__(self):
+        return {f.name: getattr(self, f.name) for f in dataclasses.fields(self)}
 
     @functools.cached_property
     def _ref(self):

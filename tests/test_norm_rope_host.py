@@ -1,7 +1,10 @@
 """Host-side checks of the norm + rotation and 8-bit checkpoint calls: every
 refusal happens before anything is launched (no GPU needed), and the plain
 forms that the GPU tests compare with are themselves checked."""
+import copy
 import ctypes
+import dataclasses
+import pickle
 
 import numpy as np
 import pytest
@@ -210,6 +213,15 @@ def test_binding_refuses_before_the_call():
         V.qk_norm_rope(sh, None, qkv, t, t, t)
     with pytest.raises(V.VmobaError, match="SHAPE"):
         V.qk_norm_rope(_shape(bt=3), nr, qkv, t, t, t)
+
+
+def test_a_used_shape_is_copied_and_pickled():
+    sh = _shape()
+    assert sh._native is not None and sh._ref is not None
+    for other in (copy.deepcopy(sh), pickle.loads(pickle.dumps(sh)),
+                  dataclasses.replace(sh, n_heads=2)):
+        assert other == sh and hash(other) == hash(sh) and "_native" not in other.__dict__
+        assert other._native is not sh._native
 
 
 def test_rope_dims():
