@@ -370,6 +370,9 @@ __device__ __forceinline__ uint2 encode8(const Vals& v, uint32_t m, float& scale
     const bool bad = m >= 0x7F800000u, none = m < kLow;
     if (bad) scale = __uint_as_float(0x7FC00000u);
     if (none) scale = 0.f;
+    // the largest fp32 number: 127 a / 127 must not read back as infinite
+    if (!bad && scale * 127.0f > 0x1.fffffep127f)
+      scale = __uint_as_float(__float_as_uint(scale) - 1u);
     const float down = m > kHigh ? 0x1p-8f : 1.0f;
     const float by = __fdividef(127.0f, a * down) * down;
 #pragma unroll

@@ -405,7 +405,8 @@ int vmoba_qk_norm_rope_bwd_act8(const vmoba_shape* shape, const vmoba_norm_rope*
  * elements apart (ld >= cols; any alignment of the type).  Groups of `group`
  * (64 or 128) neighbouring columns, the last of a row possibly short: with a =
  * max |x| of the group, codes = round-half-even(127 x / a) of the exact
- * quotient, scales = a / 127 in fp32.  A group that holds an infinity or a NaN
+ * quotient, scales = a / 127 in fp32 (one step less where 127 times that is
+ * beyond fp32's range).  A group that holds an infinity or a NaN
  * gets a NaN scale, one with a < 2^-119 a zero scale; their codes are zero.
  * codes: [rows][cols] int8, scales: [rows][ceil(cols / group)] fp32, 4-byte
  * aligned.  rows >= 0, cols >= 1, rows * ceil(cols / group) < 2^34. */

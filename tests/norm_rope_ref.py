@@ -100,6 +100,9 @@ def encode8(x, group):
     use = np.where(bad | small, 1.0, a)
     codes = np.rint(np.where((bad | small)[..., None], 0.0, 127.0 * pad) / use[..., None])
     scales = (use.astype(np.float32) / np.float32(127.0)).astype(np.float32)
+    with np.errstate(over="ignore"):       # 127 scale must not read back as infinite
+        over = np.isinf(scales * np.float32(127.0))
+    scales[over] = np.nextafter(scales[over], np.float32(0.0))
     scales[small] = 0.0
     scales[bad] = np.nan
     return codes.reshape(x.shape[:-1] + (n * group,))[..., :cols].astype(np.int8), scales

@@ -92,12 +92,14 @@ def test_extremes(dtype):
     x[9, :] = 0.0
     x[9, 255] = 5.0
     x[10] = -1.0
+    x[11, ::2] = torch.finfo(x.dtype).max
     for group in (64, 128):
         _check(x, group)
     ckpt, out = _roundtrip(x, 64)
     assert torch.isnan(out[1, :64]).all() and torch.isfinite(out[1, 64:]).all()
     assert torch.isnan(out[2, 192:]).all() and torch.isfinite(out[2, :192]).all()
     assert (out[7] == 0).all() and (out[6] != 0).all()
+    assert torch.isfinite(out[11]).all()
 
 
 def test_more_axes_no_rows_and_padding_kept():
