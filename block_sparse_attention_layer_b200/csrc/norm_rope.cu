@@ -10,9 +10,9 @@
 // Bound: HBM.  Each raw value is read once, each result written once: 6 s n_h d
 // elements (3 of them 1.03 bytes when they come from codes, 3.1 s n_h d bytes
 // more when a checkpoint is written).  55296 tokens, 12 heads of 128, bf16:
-// 162 us into 288 blocks (6.3 TB/s, 0.97 of a plain copy's 6.46), 176 us into
-// eight blocks, 214 us with the checkpoint written (0.93), 137 us from it
-// (0.88).
+// 161 us in token order or into 288 blocks (6.3 TB/s, 0.98 of a plain copy's
+// 6.46), 175 us into eight blocks, 214 us with the checkpoint written (0.93),
+// 137 us from it (0.88).
 //
 // A lane works on two rows of q, k and v at a time, two neighbouring heads of
 // one token where the head count is even (they share the position and its
@@ -46,7 +46,7 @@ struct Walk {
   int bt, bh, bw;                  // box of a block
   int nbh, nbw, Nb, L;
   FastDiv hw, w;                   // bh * bw, bw
-  int chunk, chunks;               // rows of a chunk, chunks of a block
+  int chunks;                      // CTAs that share a block's rows
   int up;                          // units of heads of a CTA
   uint32_t ld, q_tok, kv_tok;      // bytes between tokens of the raw rows and q; positions of k, v
   long long kv_head;               // elements between heads of k and v
@@ -152,12 +152,12 @@ k_norm_rope(const __grid_constant__ Walk w, const __grid_constant__ NormRopeArgs
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane / G, l = lane % G;
   const int h0 = (blockIdx.y * w.up + warp % w.up) * NA;
-  // partition order: chunk x of block z; token order: chunk z
+  // partition order: chunk x of block z; token order: chunk z.  The chunks of a
+  // block are interleaved strides of its rows, so that their CTAs walk one
+  // window of it together (1 to 3 % faster than stretches of their own).
   const int j = o.blocks ? blockIdx.z : 0;
-  const int first = (o.blocks ? blockIdx.x : blockIdx.z) * w.chunk;
-  const int last = min(first + w.chunk, w.L);
-  const int step = kWarps / w.up * R;
-
+  const int step = kWarps / w.up * R, own = step * (TwoHeads ? 1 : 2);
+  const int first = (o.blocks ? blockIdx.x : blockIdx.z) * own, last = w.L;
   after_previous();
   const Vals gq = load_weights<E, D>(a.gq, l), gk = load_weights<E, D>(a.gk, l);
   const PairRefs refs = pair_refs<E, D>(l, a.ht, a.hh, a.hw);
@@ -186,7 +186,7 @@ k_norm_rope(const __grid_constant__ Walk w, const __grid_constant__ NormRopeArgs
       }
   };
 
-  const int stride = step * (TwoHeads ? 1 : 2);
+  const int stride = own * w.chunks;
   const int r_begin = first + warp / w.up * R;
   // row r of the block is token n = (t, y, x)
   auto locate = [&](int r) {
@@ -397,21 +397,23 @@ cudaError_t launch_t(const Prob& P, const NormRopeArgs& a, const NormRopeOut& o,
     // One CTA for each block and unit of heads where these are at least one and
     // a half rounds of CTAs (1.6 rounds: 108 us against 113 of the search
     // below on 32760 tokens in 78 blocks; 5.8 rounds: 162 against 165 on 55296
-    // tokens in 288 blocks; but from codes 141 against 137).  Else the units and chunks of a CTA for which the
-    // slowest of the places that CTAs run in has the fewest steps, a CTA's
-    // filling and reducing costing about two (55296 tokens in 8 blocks: 179 us
-    // against 187 with eight chunks of two units, 433 with one CTA a block).
+    // tokens in 288 blocks; but from codes 141 against 137).  Else the units
+    // and chunks of a CTA for which the slowest of the places that CTAs run in
+    // has the fewest strides; a CTA's filling and reducing costs about two, a
+    // cluster's two more (55296 tokens in 8 blocks: 174 us against 189 with
+    // eight chunks of two units, 433 with one CTA a block; 2048 tokens of 4
+    // heads in 64 blocks: 3.2 us against 4.2 with clusters of two).
     w.up = w.chunks = 1;
     long long best = -1;
     const bool many = !From8 && 2LL * P.Nb * units >=
                                     3LL * capacity.ctas(kernel, dev, 1, M::kBytes, num_sms);
-    for (int up = units % 2 == 0 ? 2 : 1; up >= 1 && !many; --up) {
-      const int step = kWarps / up * R;
-      for (int c = 1; c <= 8 && c <= P.L; ++c) {
+    for (int up = 1; up <= (units % 2 ? 1 : 2) && !many; ++up) {
+      const int own = kWarps / up * R * (TwoHeads ? 1 : 2), strides = (P.L + own - 1) / own;
+      for (int c = 1; c <= 8 && c <= strides; ++c) {
         const long long ctas = (long long)P.Nb * c * (units / up);
         const int slots = capacity.ctas(kernel, dev, c, M::kBytes, num_sms);
         const long long cost =
-            ((ctas + slots - 1) / slots) * (((P.L + c - 1) / c + step - 1) / step + 2);
+            ((ctas + slots - 1) / slots) * ((strides + c - 1) / c + (c > 1 ? 4 : 2));
         if (best < 0 || cost < best) {
           best = cost;
           w.up = up;
@@ -419,19 +421,17 @@ cudaError_t launch_t(const Prob& P, const NormRopeArgs& a, const NormRopeOut& o,
         }
       }
     }
-    w.chunk = (P.L + w.chunks - 1) / w.chunks;
   } else {                             // token order: one block that is the whole latent
     w.bt = P.T; w.bh = P.H; w.bw = P.W;
     w.nbh = w.nbw = w.Nb = 1;
     w.L = P.s;
     w.kv_tok = P.n_h * D * sizeof(E);
     w.kv_head = D;
+    // eight CTAs an SM (11520 tokens: 36.5 us; two 40.9, sixteen 36.6, 32 43.8)
     w.up = units % 2 == 0 ? 2 : 1;
-    const int step = kWarps / w.up * R;
-    const long long want = 8LL * num_sms * w.up / units + 1;
-    w.chunk = (int)((P.s + want - 1) / want);
-    w.chunk = (w.chunk + step - 1) / step * step;
-    w.chunks = (P.s + w.chunk - 1) / w.chunk;
+    const int own = kWarps / w.up * R * (TwoHeads ? 1 : 2);
+    const long long strides = (P.s + own - 1) / own, want = 8LL * num_sms * w.up / units + 1;
+    w.chunks = (int)(strides < want ? strides : want);
   }
   w.hw = FastDiv(w.bh * w.bw);
   w.w = FastDiv(w.bw);

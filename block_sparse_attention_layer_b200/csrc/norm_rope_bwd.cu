@@ -7,19 +7,15 @@
 // the codes, whose squares sum to an exact integer, without their scales).
 //
 // Bound: HBM, 8 s n_h d elements (two of them 1.03 bytes when x is a
-// checkpoint).  12 heads of 128, bf16: 75600 tokens 293 to 328 us from one card
-// to another (0.98 to 0.88 of a plain copy's rate; a higher SM clock makes it 1
-// to 2 % slower, and fewer instructions a step made it no faster), 55296 tokens
-// from a checkpoint 194 to 209 us.
+// checkpoint).  12 heads of 128, bf16: 75600 tokens 289 to 295 us (0.97 to 0.99
+// of a plain copy's 6.46 TB/s), 55296 tokens 211 us, or from a checkpoint 194 to
+// 205 us (0.91 to 0.95; 2.4 instructions a cycle and SM).
 //
 // As in the forward, a lane works on two rows of q, k (and v) at a time, two
 // neighbouring heads of a token where the head count is even, fed through
-// shared memory by asynchronous copies one step ahead (three steps in shared
-// memory: 233 us against 223).  CTAs stay resident and walk items of
-// neighbouring tokens of one unit of heads; neighbouring items are the units
-// of the same tokens, so that whole rows pass at one time (a warp taking all
-// of its tokens' heads one after another instead: 229 us against 209 from a
-// checkpoint).  Each lane keeps fp32 sums of its weight gradients over at most
+// shared memory by asynchronous copies one step ahead.  CTAs stay resident and
+// walk items of neighbouring tokens of one unit of heads; neighbouring items
+// are the units of the same tokens, so that whole rows pass at one time.  Each lane keeps fp32 sums of its weight gradients over at most
 // kFlush rows and adds them to fp64 sums in shared memory, the CTA's total goes
 // to the workspace, and a second kernel adds the totals in a fixed order, so
 // results do not depend on scheduling.
@@ -87,8 +83,7 @@ struct Smem {
       kRing + kSpots + 16 * kLanes * (int)sizeof(double) + 2 * D * (int)sizeof(float);
 };
 
-// The weights of q and k (2 D) in shared memory (16 registers a lane fewer; 306
-// -> 293 us for 75600 tokens): a lane's first four and last four elements lie
+// The weights of q and k (2 D) in shared memory, 16 registers a lane fewer: a lane's first four and last four elements lie
 // in separate halves, for 16-byte reads without bank conflicts.
 template <typename E, int D>
 __device__ __forceinline__ void place_weight(const NormRopeArgs& a, int c, float* to) {
@@ -138,8 +133,7 @@ k_norm_rope_bwd(const __grid_constant__ Walk w, const __grid_constant__ NormRope
   }
 
   // A warp walks the tokens of its CTA's items as one sequence, so that its
-  // loads run ahead over the end of an item too (all warps of a CTA taking all
-  // steps together: 325 us against 305 on 75600 tokens).
+  // loads run ahead over the end of an item too.
   struct At {
     int item, n0, last, h0;
   };
@@ -335,14 +329,17 @@ cudaError_t launch_t(const Prob& P, const NormRopeArgs& a, const void* dq, const
   w.w = FastDiv(P.W);
   w.ld = (uint32_t)(a.ld * sizeof(E));
   w.ld_out = (uint32_t)(ld_out * sizeof(E));
-  // items of up to 32 strides of the CTA's warps, of the length for which the
-  // CTA with the most items has the fewest strides (55296 tokens of 12 heads:
-  // four items of 18 where 4.4 of 16 left a tenth of the CTAs' time unused)
+  // Items are strides of the CTA's warps.  From raw rows one each: the CTAs then
+  // walk one window of neighbouring rows together, where longer items keep each
+  // CTA on a distance of its own from the next, which DRAM takes badly (75600
+  // tokens: 290 us with one, 306 with two, 318 with eight, 327 with 32).  From
+  // codes up to 32, of the length for which the CTA with the most items has the
+  // fewest strides (267 us; 279 with one).
   constexpr int stride = kWarps * (256 / D) * (TwoHeads ? 1 : 2);
   const int units = TwoHeads ? P.n_h / 2 : P.n_h, slots = min(2 * num_sms, kMaxCtas);
   const long long strides = (P.s + stride - 1) / stride;
   long long best = -1;
-  for (int k = 32; k >= 1; --k) {
+  for (int k = From8 ? 32 : 1; k >= 1; --k) {
     const long long items = (strides + k - 1) / k * units, most = (items + slots - 1) / slots * k;
     if (best < 0 || most < best) {
       best = most;
