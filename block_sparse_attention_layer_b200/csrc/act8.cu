@@ -68,8 +68,7 @@ __device__ __forceinline__ Place place(const Shape& s, long long row0, int g0, i
 
 template <typename E, int Group, bool Vec, int U>
 __global__ void __launch_bounds__(kThreads)
-k_act8_pack(const E* __restrict__ x, const __grid_constant__ Shape s, int8_t* __restrict__ codes,
-            float* __restrict__ scales) {
+k_act8_pack(const E* x, const __grid_constant__ Shape s, int8_t* codes, float* scales) {
   constexpr int G = Group / 8, kPer = kThreads / G;
   const int l = threadIdx.x % G;
   const long long base = (long long)blockIdx.x * (U * kPer);
@@ -128,8 +127,8 @@ k_act8_pack(const E* __restrict__ x, const __grid_constant__ Shape s, int8_t* __
 
 template <typename E, int Group, bool Vec, int U>
 __global__ void __launch_bounds__(kThreads)
-k_act8_unpack(const int8_t* __restrict__ codes, const float* __restrict__ scales,
-              const __grid_constant__ Shape s, E* __restrict__ out) {
+k_act8_unpack(const int8_t* codes, const float* scales,
+              const __grid_constant__ Shape s, E* out) {
   constexpr int G = Group / 8, kPer = kThreads / G;
   const int l = threadIdx.x % G;
   const long long base = (long long)blockIdx.x * (U * kPer);
@@ -145,12 +144,12 @@ k_act8_unpack(const int8_t* __restrict__ codes, const float* __restrict__ scales
     const int k = min(u * kPer + (int)threadIdx.x / G, most - 1);
     at[u] = place(s, row0, g0, k);
     at[u].c0 *= Group;
-    scale[u] = __ldg(scales + base + k);
+    scale[u] = scales[base + k];
     const int8_t* src = codes + at[u].row * s.cols;
     if constexpr (Vec) {
       const int c = at[u].c0 + l * 8;
       w[u] = make_uint2(0u, 0u);
-      if (c < s.cols) w[u] = __ldg(reinterpret_cast<const uint2*>(src + c));
+      if (c < s.cols) w[u] = *reinterpret_cast<const uint2*>(src + c);
     } else {
       uint32_t b[2] = {0u, 0u};
 #pragma unroll

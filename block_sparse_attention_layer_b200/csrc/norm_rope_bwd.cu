@@ -15,10 +15,11 @@
 // neighbouring heads of a token where the head count is even, fed through
 // shared memory by asynchronous copies one step ahead.  CTAs stay resident and
 // walk items of neighbouring tokens of one unit of heads; neighbouring items
-// are the units of the same tokens, so that whole rows pass at one time.  Each lane keeps fp32 sums of its weight gradients over at most
-// kFlush rows and adds them to fp64 sums in shared memory, the CTA's total goes
-// to the workspace, and a second kernel adds the totals in a fixed order, so
-// results do not depend on scheduling.
+// are the units of the same tokens, so that whole rows pass at one time.  Each
+// lane keeps fp32 sums of its weight gradients over at most kFlush rows and
+// adds them to fp64 sums in shared memory, the CTA's total goes to the
+// workspace, and a second kernel adds the totals in a fixed order, so results
+// do not depend on scheduling.
 #include "rows.cuh"
 
 namespace vmoba {
@@ -83,13 +84,14 @@ struct Smem {
       kRing + kSpots + 16 * kLanes * (int)sizeof(double) + 2 * D * (int)sizeof(float);
 };
 
-// The weights of q and k (2 D) in shared memory, 16 registers a lane fewer: a lane's first four and last four elements lie
-// in separate halves, for 16-byte reads without bank conflicts.
+// The weights of q and k (2 D) in shared memory, 16 registers a lane fewer: a
+// lane's first four and last four elements lie in separate halves, for 16-byte
+// reads without bank conflicts.
 template <typename E, int D>
 __device__ __forceinline__ void place_weight(const NormRopeArgs& a, int c, float* to) {
   const float* g = c < D ? a.gq : a.gk;
   const int half = c % D / (D / 2), l = c % (D / 2) / 4;
-  to[c] = g ? __ldg(g + elem_at<E, D>(l, half * 4 + c % 4)) : 1.f;
+  to[c] = g ? g[elem_at<E, D>(l, half * 4 + c % 4)] : 1.f;
 }
 template <int D>
 __device__ __forceinline__ Vals weights(const float* g, int l) {
@@ -107,8 +109,7 @@ __device__ __forceinline__ unsigned long long offset(int n, uint32_t stride, uin
 template <typename E, int D, bool From8, bool TwoHeads>
 __global__ void __launch_bounds__(kThreads, 2)
 k_norm_rope_bwd(const __grid_constant__ Walk w, const __grid_constant__ NormRopeArgs a,
-                const E* __restrict__ dq, const E* __restrict__ dk, const E* __restrict__ dv,
-                E* __restrict__ oq, E* __restrict__ ok, E* __restrict__ ov, float* part) {
+                const E* dq, const E* dk, const E* dv, E* oq, E* ok, E* ov, float* part) {
   constexpr int G = D / 8, R = 32 / G, S = kStages;
   constexpr int kStep = kWarps * R, kStride = kStep * (TwoHeads ? 1 : 2);
   using F = Feed<E, D, From8, TwoHeads>;
@@ -303,14 +304,14 @@ k_norm_rope_bwd(const __grid_constant__ Walk w, const __grid_constant__ NormRope
 // The CTAs' totals added up: 32 columns a block, 32 threads a column, each
 // over every 32nd CTA, and their sums in order.
 __global__ void __launch_bounds__(1024)
-k_norm_dweight(const float* __restrict__ part, int n, int cols, float* __restrict__ out) {
+k_norm_dweight(const float* part, int n, int cols, float* out) {
   __shared__ double sums[32][33];
   const int c = threadIdx.x & 31, k = threadIdx.x >> 5;
   after_previous();
   const float* p = part + blockIdx.x * 32 + c;
   double sum = 0.0;
 #pragma unroll 8
-  for (int i = k; i < n; i += 32) sum += (double)__ldg(p + (size_t)i * cols);
+  for (int i = k; i < n; i += 32) sum += (double)p[(size_t)i * cols];
   sums[k][c] = sum;
   __syncthreads();
   if (k == 0) {

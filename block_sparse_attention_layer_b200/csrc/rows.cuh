@@ -59,7 +59,7 @@ __device__ __forceinline__ int elem_at(int l, int i) {
 // Values pass once: no place in L1.
 __device__ __forceinline__ uint4 load16(const void* p) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
 }
@@ -257,7 +257,10 @@ __device__ __forceinline__ float lane_dot(const Vals& a, const Vals& b) {
 
 // Waits until the stream's previous kernel has finished and its writes are
 // visible (every access to global memory comes after this), and lets the next
-// one be set up once all of this grid's CTAs run.
+// one be set up once all of this grid's CTAs run.  Global memory is read by
+// plain loads only: a read-only one (__ldg, or through a const __restrict__
+// parameter) holds its data to be constant for as long as the kernel lives,
+// which begins before this, and may be moved up across it.
 __device__ __forceinline__ void after_previous() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -553,10 +556,10 @@ __device__ __forceinline__ void load_turns(const PairRefs& r, const float2* tabl
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       cs[i] = r.still >> i & 1u ? make_float2(1.f, 0.f)
-                                : __ldg(table + spot->row[r.axis[i]] + r.place[i]);
+                                : table[spot->row[r.axis[i]] + r.place[i]];
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) cs[i] = __ldg(table + spot->row[r.axis[i]] + r.place[i]);
+    for (int i = 0; i < 4; ++i) cs[i] = table[spot->row[r.axis[i]] + r.place[i]];
   }
 }
 
@@ -582,7 +585,7 @@ template <typename E, int D>
 __device__ __forceinline__ Vals load_weights(const float* g, int l) {
   Vals w;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) w.at(i) = g ? __ldg(g + elem_at<E, D>(l, i)) : 1.f;
+  for (int i = 0; i < 8; ++i) w.at(i) = g ? g[elem_at<E, D>(l, i)] : 1.f;
   return w;
 }
 

@@ -436,3 +436,51 @@ def test_refusals_leave_outputs_alone():
     torch.cuda.synchronize()
     assert V.kernel_launches() == n0
     assert all((t == 9.0).all() for t in out)
+
+
+@pytest.mark.parametrize("grid,h,d", [((2, 3, 5), 2, 64), ((9, 16, 17), 4, 128)])
+def test_chain_reads_what_the_last_call_wrote(grid, h, d):
+    """Calls behind one another on a stream, each set up while the one before
+    still runs: weights, rows, codes and scales are what that one wrote into
+    buffers that held other values before, bit for bit as with waits between."""
+    c = Case(grid, h, d, "bf16", seed=21)
+    gen = torch.Generator(device="cuda").manual_seed(22)
+    n, u = 12, (c.s, 3, c.h, c.d)
+    weights = [V.Act8.empty((2, d), d) for _ in range(n)]
+    rows = [V.Act8.empty(u, d) for _ in range(n)]
+    for w, r in zip(weights, rows):
+        V.act8_pack(1 + torch.randn((2, d), generator=gen, device="cuda"), w)
+        V.act8_pack(torch.randn(u, generator=gen, device="cuda").to(c.dt), r)
+    g = torch.zeros((2, d), device="cuda")
+    raw = torch.zeros(u, dtype=c.dt, device="cuda")
+    ckpt = V.Act8.empty(u, d)
+    ws = torch.zeros(V.qk_norm_rope_bwd_workspace_size(c.sh), dtype=torch.uint8, device="cuda")
+    nr = V.NormRope(g[0], g[1], c.eps, c.table, c.dims)
+
+    def chain(between):
+        outs = []
+        for w, r in zip(weights, rows):
+            first, second, grads = ([c.token() for _ in range(3)] for _ in range(3))
+            d_raw, d_raw8 = torch.empty_like(raw), torch.empty_like(raw)
+            dw, dw8 = torch.empty_like(g), torch.empty_like(g)
+            between()
+            for call in (
+                    lambda: V.act8_unpack(r, raw),
+                    lambda: V.act8_unpack(w, g),
+                    lambda: V.qk_norm_rope(c.sh, nr, raw, *first, ckpt=ckpt),
+                    lambda: V.qk_norm_rope(c.sh, nr, ckpt, *second),
+                    lambda: V.qk_norm_rope_bwd(c.sh, nr, raw, *second, d_raw, dw, ws),
+                    lambda: V.qk_norm_rope_bwd(c.sh, nr, ckpt, *first, d_raw8, dw8, ws),
+                    lambda: V.act8_pack(d_raw8, ckpt),
+                    lambda: V.act8_unpack(ckpt, raw),
+                    lambda: V.qk_norm_rope(c.sh, nr, raw, *grads)):
+                call()
+                between()
+            outs.append([*first, *second, *grads, d_raw, d_raw8, dw, dw8])
+        torch.cuda.synchronize()
+        return outs
+
+    want = chain(torch.cuda.synchronize)
+    for _ in range(3):
+        for a, b in zip(chain(lambda: None), want):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
