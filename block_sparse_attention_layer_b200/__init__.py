@@ -2,10 +2,11 @@
 
 The compute path is libvmoba.so (CUDA, sm_100a) behind the C ABI declared in
 include/vmoba.h; this package is its Python binding (``_lib``; ``norm_rope``
-for what stands around the attention), a buffer-owning per-layer driver (``layer``), the in-tree build script (``build``) and
-the bench's FLOP-count convention (``metrics``) and the split of a layer's
-heads across GPUs (``sharding``).  Importing the package does
-not load the library; the first ABI call does, and raises if it is missing.
+for what stands around the attention), a buffer-owning per-layer driver
+(``layer``), the in-tree build script (``build``), the bench's FLOP-count
+convention (``metrics``) and the split of a layer's heads across GPUs
+(``sharding``).  Importing the package does not load the library; the first ABI
+call does, and raises if it is missing.
 """
 from ._lib import (  # noqa: F401
     LayerShape, VmobaError, lib, mode_for_layer, num_blocks, workspace_size,
