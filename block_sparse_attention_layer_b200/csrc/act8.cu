@@ -185,7 +185,7 @@ template <typename E, int Group, typename F>
 cudaError_t with_shape(const void* x, long long n_rows, int cols, long long ld,
                        const int8_t* codes, int num_sms, F f) {
   Shape s{};
-  s.per_row = (cols + Group - 1) / Group;
+  s.per_row = (int)(((long long)cols + Group - 1) / Group);    // cols may be the largest int
   s.cols = cols;
   s.ld = ld;
   s.n_groups = n_rows * s.per_row;

@@ -158,3 +158,34 @@ def test_offsets_beyond_32_bits():
     V.act8_unpack(tail, out)
     V.act8_unpack(ckpt, x)
     assert torch.equal(x[-1000:], out)
+
+
+@pytest.mark.parametrize("cols", [2 ** 31 - 128, 2 ** 31 - 8, 2 ** 31 - 1])
+@pytest.mark.parametrize("group", [64, 128])
+def test_widest_rows(cols, group):
+    """One row of nearly 2^31 values: its whole groups are those of the same
+    values as rows of one group, the short last one the plain form's."""
+    x = torch.empty((1, cols), dtype=torch.bfloat16, device="cuda")
+    part = torch.randn(2 ** 24 + 1, device="cuda").to(torch.bfloat16)
+    for i in range(0, cols, part.numel()):
+        x[0, i:i + part.numel()] = (part * (1 + i // part.numel()))[:cols - i]
+    ckpt = V.Act8.empty((1, cols), group)
+    V.act8_pack(x, ckpt)
+    whole = cols // group * group
+    rows = V.Act8.empty((whole // group, group), group)
+    V.act8_pack(x[0, :whole].view(-1, group), rows)
+    assert torch.equal(ckpt.codes[0, :whole], rows.codes.view(-1))
+    assert torch.equal(ckpt.scales[0, :whole // group], rows.scales.view(-1))
+    last = x[:, -1000:].double().cpu().numpy()[:, -(cols - whole):] if cols > whole else None
+    out = torch.empty_like(x)
+    V.act8_unpack(ckpt, out)
+    del x
+    want = torch.empty((whole // group, group), dtype=out.dtype, device="cuda")
+    V.act8_unpack(rows, want)
+    assert torch.equal(out[0, :whole], want.view(-1))
+    if last is not None:
+        codes, scales = R.encode8(last, group)
+        assert np.array_equal(ckpt.codes[:, whole:].cpu().numpy(), codes)
+        assert np.array_equal(ckpt.scales[:, -1:].cpu().numpy(), scales)
+        back = torch.from_numpy(R.decode8(codes, scales, group)).to(out.dtype)
+        assert torch.equal(out[:, whole:].cpu(), back)

@@ -4,7 +4,10 @@ forms that the GPU tests compare with are themselves checked."""
 import copy
 import ctypes
 import dataclasses
+import os
 import pickle
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -255,3 +258,25 @@ def test_plain_rotation_is_the_stated_one():
                 want += [0.0] * (d // 2 - len(want))
                 got = z[(t * H + y) * W + x]
                 assert np.allclose(got, np.exp(1j * np.array(want)), atol=1e-12)
+
+
+_WIDEST = """
+import ctypes, sys
+import block_sparse_attention_layer_b200 as V
+L, p = V.lib(), ctypes.c_void_p(0x100000)
+for cols in (2 ** 31 - 128, 2 ** 31 - 127, 2 ** 31 - 64, 2 ** 31 - 63, 2 ** 31 - 8, 2 ** 31 - 1):
+    for group in (64, 128):
+        for dtype in (0, 1):
+            print(L.vmoba_act8_pack(dtype, p, 1, cols, cols, group, p, p, None),
+                  L.vmoba_act8_unpack(dtype, p, p, 1, cols, group, p, cols, None))
+"""
+
+
+def test_act8_takes_the_widest_rows():
+    """Rows up to the widest that an int counts reach the launch, which fails
+    here for want of a device (none is visible to the process)."""
+    env = dict(os.environ, CUDA_VISIBLE_DEVICES="")
+    done = subprocess.run([sys.executable, "-c", _WIDEST], env=env, timeout=100, text=True,
+                          capture_output=True, cwd=os.path.dirname(os.path.dirname(__file__)))
+    assert done.returncode == 0, done.stderr
+    assert done.stdout.split() == ["-5"] * 48
