@@ -85,15 +85,22 @@ void expect_type(PyObject* o, at::ScalarType type, const char* name) {
 }
 
 // A call's tensors, whose devices are compared once everything else is right.
+// Each is held until the call has returned: an attribute of an argument may be
+// a tensor made for this one access.
 struct Device {
-  struct Seen { const at::Tensor* t; const char *name, *part; } seen[16];
+  struct Seen { PyObject* o; const char *name, *part; } seen[16];
   int n = 0, index = -1;
-  void take(const at::Tensor& t, const char* name, const char* part = "") {
-    seen[n++] = {&t, name, part};      // at most 13 in a call
+  Device() = default;
+  Device(const Device&) = delete;
+  Device& operator=(const Device&) = delete;
+  ~Device() { while (n) Py_DECREF(seen[--n].o); }
+  void take(PyObject* o, const char* name, const char* part = "") {
+    Py_INCREF(o);
+    seen[n++] = {o, name, part};       // at most 13 in a call
   }
   void settle() {
     for (int i = 0; i < n; ++i) {
-      const at::Tensor& t = *seen[i].t;
+      const at::Tensor& t = THPVariable_Unpack(seen[i].o);
       if (i == 0 && t.is_cuda()) index = t.get_device();
       if (t.is_cuda() && t.get_device() == index) continue;
       const std::string name = std::string(seen[i].name) + seen[i].part;
@@ -117,7 +124,7 @@ void* at_(PyObject* o, std::initializer_list<int64_t> size, at::ScalarType type,
   expect_size(t, size, name);
   expect_type(o, type, name);
   if (!t.is_contiguous()) refuse(std::string(name) + ": expected a contiguous tensor");
-  d.take(t, name);
+  d.take(o, name);
   return t.data_ptr();
 }
 
@@ -178,16 +185,15 @@ Raw raw_rows(const Shape& sh, PyObject* o, Device& dev, const char* name) {
         refuse(std::string(name) + ": expected one token stride, got " + std::to_string(r.ld) +
                " and " + std::to_string(ld));
       r.at[i] = t.data_ptr();
+      dev.take(item, name);
     }
-    for (int i = 0; i < 3; ++i)
-      dev.take(THPVariable_Unpack(PySequence_Fast_GET_ITEM(o, i)), name);
     return r;
   }
   const at::Tensor& t = tensor(o, name);
   expect_size(t, {sh.s, 3, sh.h, sh.d}, name);
   expect_type(o, sh.type, name);
   r.ld = token_stride(t, 3 * row, name);
-  dev.take(t, name);
+  dev.take(o, name);
   for (int i = 0; i < 3; ++i)
     r.at[i] = static_cast<char*>(t.data_ptr()) + i * row * (int64_t)t.element_size();
   return r;
@@ -226,8 +232,8 @@ Ckpt checkpoint(PyObject* o, at::IntArrayRef size, int64_t group, Device& dev, c
     expect_type(x.o, x.type, part.c_str());
     refuse(part + ": expected a contiguous tensor");
   }
-  dev.take(tc, name, ".codes");
-  dev.take(ts, name, ".scales");
+  dev.take(codes.p, name, ".codes");
+  dev.take(scales.p, name, ".scales");
   c.codes = static_cast<int8_t*>(tc.data_ptr());
   c.scales = static_cast<float*>(ts.data_ptr());
   return c;
@@ -374,7 +380,7 @@ PyObject* backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
       dw = static_cast<float*>(at_(a[7], {2, sh.d}, at::kFloat, dev, "dweight"));
       const at::Tensor& t = tensor(a[8], "ws");
       if (!t.is_contiguous()) refuse("ws: expected a contiguous tensor");
-      dev.take(t, "ws");
+      dev.take(a[8], "ws");
       ws = t.data_ptr();
       ws_bytes = t.nbytes();
     }
@@ -416,7 +422,7 @@ PyObject* act8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     if (cols > INT32_MAX) refuse(std::string(name) + ": too many columns");
     Device dev;
-    dev.take(t, name);
+    dev.take(a[1], name);
     const Ckpt c = checkpoint(a[2], t.sizes(), 0, dev, "ckpt");
     const cudaStream_t st = stream_of(a[3], dev);
     return call(dev, [&] {

@@ -1,6 +1,8 @@
 """Norm + rotation of queries and keys (forward in token and partition order,
 backward) against plain fp64 forms, on values, odd sizes, strides, extreme
 inputs, checkpoints, streams and graphs.  Bounds: norm_rope_ref."""
+import weakref
+
 import numpy as np
 import pytest
 
@@ -484,3 +486,41 @@ def test_chain_reads_what_the_last_call_wrote(grid, h, d):
     for _ in range(3):
         for a, b in zip(chain(lambda: None), want):
             assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_weights_made_at_each_access_live_through_the_call():
+    """A norm whose tensors are made when they are read: still alive when the
+    last of a call's arguments is read, and what the call computes with."""
+    c = Case((3, 4, 5), 2, 64, "bf16", seed=71)
+    made, alive = [], []
+
+    def fresh(t):
+        t = t.clone()
+        made.append(weakref.ref(t))
+        return t
+
+    class Norm:
+        q_weight = property(lambda self: fresh(c.gq))
+        k_weight = property(lambda self: fresh(c.gk))
+        table = property(lambda self: fresh(c.table))
+        eps, dims = c.eps, c.dims
+
+    class Stream:                      # read after every tensor
+        cuda_stream = property(lambda self: torch.cuda.current_stream().cuda_stream)
+
+        @property
+        def device(self):
+            alive.append([r() is not None for r in made])
+            return torch.device("cuda", torch.cuda.current_device())
+
+    out = [c.token(), c.token(), c.token()]
+    V.qk_norm_rope(c.sh, Norm(), c.qkv, *out, stream=Stream())
+    made.clear()
+    assert all(torch.equal(a, b) for a, b in zip(out, c.forward()))
+    _, want, dw = c.backward()
+    whole, raw = c.buffer()
+    got = torch.empty_like(dw)
+    ws = torch.empty((V.qk_norm_rope_bwd_workspace_size(c.sh),), dtype=torch.uint8, device="cuda")
+    V.qk_norm_rope_bwd(c.sh, Norm(), c.qkv, *c.grads, raw, got, ws, stream=Stream())
+    assert all(torch.equal(a, b) for a, b in zip(c.parts(raw), want)) and torch.equal(got, dw)
+    assert alive == [[True] * 3] * 2

@@ -4,10 +4,12 @@ forms that the GPU tests compare with are themselves checked."""
 import copy
 import ctypes
 import dataclasses
+import gc
 import os
 import pickle
 import subprocess
 import sys
+import weakref
 
 import numpy as np
 import pytest
@@ -280,3 +282,44 @@ def test_act8_takes_the_widest_rows():
                           capture_output=True, cwd=os.path.dirname(os.path.dirname(__file__)))
     assert done.returncode == 0, done.stderr
     assert done.stdout.split() == ["-5"] * 48
+
+
+def test_a_call_holds_its_tensors():
+    """Tensors that an argument makes anew at each access live as long as the
+    call that was given them."""
+    sh = _shape()
+    size, d = (sh.s, 3, 2, 64), 64
+    made = []
+
+    def fresh(*a, **kw):
+        t = torch.zeros(*a, **kw)
+        made.append(weakref.ref(t))
+        return t
+
+    class Made(V.Act8):
+        codes = property(lambda self: fresh(size, dtype=torch.int8))
+        scales = property(lambda self: fresh(size[:3] + (1,)))
+        group = d
+
+        def __init__(self):
+            pass
+
+    class Seen(Exception):
+        pass
+
+    class Norm:                        # its attributes are read after the rows
+        @property
+        def dims(self):
+            raise Seen([r() is not None for r in made])
+
+    t = torch.zeros((sh.s, 2, d), dtype=torch.bfloat16)
+    out = torch.zeros(size, dtype=torch.bfloat16)
+    for call in (lambda: V.qk_norm_rope(sh, Norm(), Made(), t, t, t),
+                 lambda: V.qk_norm_rope_bwd(sh, Norm(), Made(), t, t, t, out, None, None)):
+        made.clear()
+        with pytest.raises(Seen) as e:
+            call()
+        assert e.value.args[0] == [True, True]
+        del e
+        gc.collect()
+        assert [r() for r in made] == [None, None]
