@@ -88,22 +88,23 @@ void expect_type(PyObject* o, at::ScalarType type, const char* name) {
 // Each is held until the call has returned: an attribute of an argument may be
 // a tensor made for this one access.
 struct Device {
-  struct Seen { PyObject* o; const char *name, *part; } seen[16];
-  int n = 0, index = -1;
+  struct Seen { PyObject* o; const char *name, *part; };
+  c10::SmallVector<Seen, 16> seen;     // 14 in a backward with separate rows and gradients
+  int index = -1;
   Device() = default;
   Device(const Device&) = delete;
   Device& operator=(const Device&) = delete;
-  ~Device() { while (n) Py_DECREF(seen[--n].o); }
+  ~Device() { for (const Seen& x : seen) Py_DECREF(x.o); }
   void take(PyObject* o, const char* name, const char* part = "") {
     Py_INCREF(o);
-    seen[n++] = {o, name, part};       // at most 13 in a call
+    seen.push_back({o, name, part});
   }
   void settle() {
-    for (int i = 0; i < n; ++i) {
-      const at::Tensor& t = THPVariable_Unpack(seen[i].o);
-      if (i == 0 && t.is_cuda()) index = t.get_device();
+    for (const Seen& x : seen) {
+      const at::Tensor& t = THPVariable_Unpack(x.o);
+      if (&x == seen.begin() && t.is_cuda()) index = t.get_device();
       if (t.is_cuda() && t.get_device() == index) continue;
-      const std::string name = std::string(seen[i].name) + seen[i].part;
+      const std::string name = std::string(x.name) + x.part;
       if (!t.is_cuda()) refuse(name + ": expected a CUDA tensor");
       refuse(name + ": expected a tensor on cuda:" + std::to_string(index) + ", got " +
              t.device().str());

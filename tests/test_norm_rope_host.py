@@ -323,3 +323,21 @@ def test_a_call_holds_its_tensors():
         del e
         gc.collect()
         assert [r() for r in made] == [None, None]
+
+
+def test_the_call_with_the_most_tensors():
+    """Separate rows and gradients, weights, table, totals and workspace: all
+    fourteen are compared, the first one named."""
+    sh = _shape()
+    bf = torch.bfloat16
+    t = [torch.zeros((sh.s, 2, 64), dtype=bf) for _ in range(9)]
+    w = [torch.ones(64) for _ in range(2)]
+    nr = V.NormRope(*w, 1e-6, torch.zeros(((4 * 24 + 8 * 20 + 8 * 20) // 2, 2)), (24, 20, 20))
+    ws = torch.zeros(V.qk_norm_rope_bwd_workspace_size(sh), dtype=torch.uint8)
+    dw = torch.zeros((2, 64))
+    every = [*t, *w, nr.table, dw, ws]
+    before = [sys.getrefcount(x) for x in every]
+    for _ in range(3):
+        with pytest.raises(ValueError, match="qkv: expected a CUDA tensor"):
+            V.qk_norm_rope_bwd(sh, nr, tuple(t[:3]), *t[3:6], tuple(t[6:]), dw, ws)
+    assert len(every) == 14 and [sys.getrefcount(x) for x in every] == before
