@@ -133,9 +133,11 @@ class VMoBANormRopeFunction(torch.autograd.Function):
 
 class Linear8Function(torch.autograd.Function):
     """y = x W^T + b, x [rows][cols] kept for the weight's gradient as an 8-bit
-    checkpoint: dx = dy W, dW = dy^T x8, db = sum dy."""
+    checkpoint: dx = dy W, dW = dy^T x8, db = sum dy.  Under autocast the
+    products of both passes are in the region's type, as the plain layer's."""
 
     @staticmethod
+    @torch.amp.custom_fwd(device_type="cuda")
     def forward(ctx, x, weight, bias):
         ckpt = Act8.empty(x.shape, 128 if x.shape[1] % 128 == 0 else 64, x.device)
         norm_rope.act8_pack(x, ckpt)
@@ -145,13 +147,15 @@ class Linear8Function(torch.autograd.Function):
 
     @staticmethod
     @once_differentiable
+    @torch.amp.custom_bwd(device_type="cuda")
     def backward(ctx, dy):
         codes, scales, weight = ctx.saved_tensors
         dx = dw = db = None
         if ctx.needs_input_grad[0]:
             dx = dy @ weight
         if ctx.needs_input_grad[1]:
-            x = torch.empty(codes.shape, dtype=ctx.x_dtype, device=codes.device)
+            dtype = dy.dtype if dy.dtype in (torch.bfloat16, torch.float32) else ctx.x_dtype
+            x = torch.empty(codes.shape, dtype=dtype, device=codes.device)
             norm_rope.act8_unpack(Act8(codes, scales, ctx.group), x)
             dw = dy.t() @ x
         if ctx.needs_input_grad[2]:

@@ -1,0 +1,67 @@
+"""The linear layer that keeps its input in 8 bits takes what the plain layer
+takes and keeps no more than its backward reads."""
+import pytest
+
+from . import norm_rope_ref as R
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():  # pragma: no cover
+    pytest.skip("needs a CUDA device", allow_module_level=True)
+
+from block_sparse_attention_layer_b200.attention import (Linear8Function,  # noqa: E402
+                                                         VMoBASelfAttention)
+
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def _stored(x, dtype):
+    """What x [rows][cols] reads back as from 8 bits."""
+    group = 128 if x.shape[1] % 128 == 0 else 64
+    codes, scales = R.encode8(x.detach().double().cpu().numpy(), group)
+    return torch.from_numpy(R.decode8(codes, scales, group)).to(dtype).cuda()
+
+
+def _tensors(rows, cols, out_cols, xt, wt, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    normal = lambda *size: torch.randn(size, generator=g, device="cuda")    # noqa: E731
+    x = normal(rows, cols).to(DT[xt]).requires_grad_(True)
+    w, b = (t.to(DT[wt]).requires_grad_(True) for t in (normal(out_cols, cols), normal(out_cols)))
+    return x, w, b, normal(rows, out_cols).to(torch.bfloat16)
+
+
+@pytest.mark.parametrize("xt,wt", [("f32", "f32"), ("f32", "bf16"), ("bf16", "f32"),
+                                   ("bf16", "bf16")])
+def test_under_autocast(xt, wt):
+    """Products in the region's type as the plain layer's, forward and
+    backward (which runs outside of the region); gradients in the type of what
+    they belong to.  dW is dy^T times the stored values in bf16."""
+    x, w, b, dy = _tensors(37, 256, 64, xt, wt)
+    with torch.autocast("cuda", dtype=torch.bfloat16):
+        y = Linear8Function.apply(x, w, b)
+        plain = torch.nn.functional.linear(x, w, b)
+    assert y.dtype == torch.bfloat16 and torch.equal(y, plain)
+    dx, dw, db = torch.autograd.grad(y, (x, w, b), dy)
+    px, _, _ = torch.autograd.grad(plain, (x, w, b), dy)
+    assert dx.dtype == x.dtype and dw.dtype == w.dtype and db.dtype == b.dtype
+    assert torch.equal(dx, px)
+    want = dy.t() @ _stored(x, x.dtype).to(torch.bfloat16)
+    assert torch.equal(dw, want.to(w.dtype))
+    # a sum of 37 bf16 values in fp32, rounded to bf16 or not at all
+    exact = dy.double().sum(0)
+    allowed = dy.double().abs().sum(0) * 37 * R.U + exact.abs() * R.STEP["bf16"]
+    assert ((db.double() - exact).abs() <= allowed).all()
+
+
+def test_module_with_fp32_tokens_under_autocast():
+    """A bf16 module on fp32 tokens: the region casts them for the projection."""
+    torch.manual_seed(0)
+    m = VMoBASelfAttention(256, 2, 4, 8, 8, 2, ((1, 8, 8), (4, 4, 4), (2, 4, 4)), qk_norm=True,
+                           rope=True, checkpoint8=True)
+    x = torch.randn((256, 256), device="cuda", requires_grad=True)
+    with torch.autocast("cuda", dtype=torch.bfloat16):
+        y = m(x)
+    y.float().square().mean().backward()
+    assert x.grad.dtype == torch.float32 and torch.isfinite(x.grad).all()
+    assert all(torch.isfinite(p.grad).all() for p in m.parameters())
