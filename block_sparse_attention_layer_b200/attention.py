@@ -132,15 +132,18 @@ class VMoBANormRopeFunction(torch.autograd.Function):
 
 
 class Linear8Function(torch.autograd.Function):
-    """y = x W^T + b, x [rows][cols] kept for the weight's gradient as an 8-bit
-    checkpoint: dx = dy W, dW = dy^T x8, db = sum dy.  Under autocast the
+    """y = x W^T + b, x [...][cols] kept for the weight's gradient as an 8-bit
+    checkpoint of its rows: dx = dy W, dW = dy^T x8, db = sum dy.  Under autocast the
     products of both passes are in the region's type, as the plain layer's."""
 
     @staticmethod
     @torch.amp.custom_fwd(device_type="cuda")
     def forward(ctx, x, weight, bias):
-        ckpt = Act8.empty(x.shape, 128 if x.shape[1] % 128 == 0 else 64, x.device)
-        norm_rope.act8_pack(x, ckpt)
+        rows = x.reshape(-1, x.shape[-1])
+        if rows.stride(1) != 1 or rows.stride(0) < rows.shape[1]:
+            rows = rows.contiguous()
+        ckpt = Act8.empty(rows.shape, 128 if rows.shape[1] % 128 == 0 else 64, x.device)
+        norm_rope.act8_pack(rows, ckpt)
         ctx.group, ctx.x_dtype = ckpt.group, x.dtype
         ctx.save_for_backward(ckpt.codes, ckpt.scales, weight)
         return torch.nn.functional.linear(x, weight, bias)
@@ -153,6 +156,7 @@ class Linear8Function(torch.autograd.Function):
         dx = dw = db = None
         if ctx.needs_input_grad[0]:
             dx = dy @ weight
+        dy = dy.reshape(-1, dy.shape[-1])
         if ctx.needs_input_grad[1]:
             dtype = dy.dtype if dy.dtype in (torch.bfloat16, torch.float32) else ctx.x_dtype
             x = torch.empty(codes.shape, dtype=dtype, device=codes.device)

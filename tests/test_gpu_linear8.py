@@ -65,3 +65,25 @@ def test_module_with_fp32_tokens_under_autocast():
     y.float().square().mean().backward()
     assert x.grad.dtype == torch.float32 and torch.isfinite(x.grad).all()
     assert all(torch.isfinite(p.grad).all() for p in m.parameters())
+
+
+@pytest.mark.parametrize("layout", ["transposed", "expanded", "every other", "padded", "axes",
+                                    "swapped axes", "one row"])
+def test_any_layout(layout):
+    """Gradients are those of the same rows laid out densely."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    normal = lambda *size: torch.randn(size, generator=g, device="cuda").bfloat16()  # noqa: E731
+    x = {"transposed": lambda: normal(192, 6).t(), "expanded": lambda: normal(1, 192).expand(6, 192),
+         "every other": lambda: normal(6, 384)[:, ::2], "padded": lambda: normal(6, 200)[:, :192],
+         "axes": lambda: normal(2, 3, 192), "swapped axes": lambda: normal(3, 2, 192).transpose(0, 1),
+         "one row": lambda: normal(192)}[layout]().requires_grad_(True)
+    w, b = normal(64, 192).requires_grad_(True), normal(64).requires_grad_(True)
+    dy = normal(*x.shape[:-1], 64)
+    y = Linear8Function.apply(x, w, b)
+    assert torch.equal(y, torch.nn.functional.linear(x, w, b))
+    dx, dw, db = torch.autograd.grad(y, (x, w, b), dy)
+    rows = x.detach().reshape(-1, 192).contiguous().requires_grad_(True)
+    flat = dy.reshape(-1, 64)
+    rx, rw, rb = torch.autograd.grad(Linear8Function.apply(rows, w, b), (rows, w, b), flat)
+    assert torch.equal(dx, rx.view(x.shape)) and torch.equal(dw, rw) and torch.equal(db, rb)
+    assert torch.equal(dw, flat.t() @ _stored(rows, torch.bfloat16))

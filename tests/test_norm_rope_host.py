@@ -341,3 +341,16 @@ def test_the_call_with_the_most_tensors():
         with pytest.raises(ValueError, match="qkv: expected a CUDA tensor"):
             V.qk_norm_rope_bwd(sh, nr, tuple(t[:3]), *t[3:6], tuple(t[6:]), dw, ws)
     assert len(every) == 14 and [sys.getrefcount(x) for x in every] == before
+
+
+def test_linear8_takes_any_layout():
+    """Transposed, expanded and spread inputs and ones with other than two axes
+    get as far as a dense one: to the device check."""
+    from block_sparse_attention_layer_b200.attention import Linear8Function
+    dense = torch.zeros((6, 64))
+    w = torch.zeros((8, 64), requires_grad=True)
+    for x in (dense, torch.zeros((64, 6)).t(), dense[:1].expand(6, 64), dense[:, :1].expand(6, 64),
+              torch.zeros((6, 128))[:, ::2], torch.zeros((6, 96))[:, :64], torch.zeros((2, 3, 64)),
+              torch.zeros((3, 2, 64)).transpose(0, 1), dense[0]):
+        with pytest.raises(ValueError, match="x: expected a CUDA tensor"):
+            Linear8Function.apply(x, w, None)
