@@ -93,6 +93,7 @@ class VMoBANormRopeFunction(torch.autograd.Function):
     def forward(ctx, qkv, q_weight, k_weight, layer: VMoBALayer, table, dims, eps: float,
                 tau: float, full: bool, scale: float, checkpoint8: bool):
         norm = NormRope(q_weight, k_weight, eps, table, dims)
+        checkpoint8 = checkpoint8 and any(ctx.needs_input_grad[:3])
         ckpt = Act8.empty(qkv.shape, layer.shape.head_dim, qkv.device) if checkpoint8 else None
         layer.prologue(qkv, norm, ckpt)
         if full:
@@ -133,34 +134,39 @@ class VMoBANormRopeFunction(torch.autograd.Function):
 
 class Linear8Function(torch.autograd.Function):
     """y = x W^T + b, x [...][cols] kept for the weight's gradient as an 8-bit
-    checkpoint of its rows: dx = dy W, dW = dy^T x8, db = sum dy.  Under autocast the
-    products of both passes are in the region's type, as the plain layer's."""
+    checkpoint of its rows: dx = dy W, dW = dy^T x8, db = sum dy.  Without a
+    gradient of W nothing is stored.  Under autocast the products of both
+    passes are in the region's type, as the plain layer's."""
 
     @staticmethod
     @torch.amp.custom_fwd(device_type="cuda")
     def forward(ctx, x, weight, bias):
-        rows = x.reshape(-1, x.shape[-1])
-        if rows.stride(1) != 1 or rows.stride(0) < rows.shape[1]:
-            rows = rows.contiguous()
-        ckpt = Act8.empty(rows.shape, 128 if rows.shape[1] % 128 == 0 else 64, x.device)
-        norm_rope.act8_pack(rows, ckpt)
-        ctx.group, ctx.x_dtype = ckpt.group, x.dtype
-        ctx.save_for_backward(ckpt.codes, ckpt.scales, weight)
+        kept = ()
+        if ctx.needs_input_grad[1]:
+            rows = x.reshape(-1, x.shape[-1])
+            if rows.stride(1) != 1 or rows.stride(0) < rows.shape[1]:
+                rows = rows.contiguous()
+            ckpt = Act8.empty(rows.shape, 128 if rows.shape[1] % 128 == 0 else 64, x.device)
+            norm_rope.act8_pack(rows, ckpt)
+            ctx.group, ctx.x_dtype = ckpt.group, x.dtype
+            kept = ckpt.codes, ckpt.scales
+        ctx.save_for_backward(weight if ctx.needs_input_grad[0] else None, *kept)
         return torch.nn.functional.linear(x, weight, bias)
 
     @staticmethod
     @once_differentiable
     @torch.amp.custom_bwd(device_type="cuda")
     def backward(ctx, dy):
-        codes, scales, weight = ctx.saved_tensors
+        weight, *kept = ctx.saved_tensors
         dx = dw = db = None
         if ctx.needs_input_grad[0]:
             dx = dy @ weight
         dy = dy.reshape(-1, dy.shape[-1])
         if ctx.needs_input_grad[1]:
             dtype = dy.dtype if dy.dtype in (torch.bfloat16, torch.float32) else ctx.x_dtype
-            x = torch.empty(codes.shape, dtype=dtype, device=codes.device)
-            norm_rope.act8_unpack(Act8(codes, scales, ctx.group), x)
+            ckpt = Act8(*kept, ctx.group)
+            x = torch.empty(ckpt.codes.shape, dtype=dtype, device=dy.device)
+            norm_rope.act8_unpack(ckpt, x)
             dw = dy.t() @ x
         if ctx.needs_input_grad[2]:
             db = dy.sum(0)

@@ -10,6 +10,8 @@ pytestmark = pytest.mark.gpu
 if not torch.cuda.is_available():  # pragma: no cover
     pytest.skip("needs a CUDA device", allow_module_level=True)
 
+import block_sparse_attention_layer_b200 as V  # noqa: E402
+from block_sparse_attention_layer_b200 import attention  # noqa: E402
 from block_sparse_attention_layer_b200.attention import (Linear8Function,  # noqa: E402
                                                          VMoBASelfAttention)
 
@@ -87,3 +89,60 @@ def test_any_layout(layout):
     rx, rw, rb = torch.autograd.grad(Linear8Function.apply(rows, w, b), (rows, w, b), flat)
     assert torch.equal(dx, rx.view(x.shape)) and torch.equal(dw, rw) and torch.equal(db, rb)
     assert torch.equal(dw, flat.t() @ _stored(rows, torch.bfloat16))
+
+
+def _module(**kw):
+    torch.manual_seed(0)
+    return VMoBASelfAttention(256, 2, 4, 8, 8, 2, ((1, 8, 8), (4, 4, 4), (2, 4, 4)), qk_norm=True,
+                              rope=True, **kw)
+
+
+def test_frozen_modules_keep_no_codes():
+    """Projection weights frozen: only the raw q, k, v are stored; everything
+    frozen: nothing, and no kernel stores them."""
+    x = torch.randn((256, 256), device="cuda").bfloat16()
+    plain, m = _module(), _module(checkpoint8=True)
+
+    def run(m, x):
+        codes, n0 = [], V.kernel_launches()
+
+        def keep(t):
+            if t.dtype == torch.int8:
+                codes.append(t.numel())
+            return t
+
+        with torch.autograd.graph.saved_tensors_hooks(keep, lambda t: t):
+            y = m(x)
+        return y, codes, V.kernel_launches() - n0
+
+    y0, none, n0 = run(plain, x)
+    y1, every, n1 = run(m, x)
+    assert torch.equal(y0, y1) and none == [] and sorted(every) == [256 * 256] * 2 + [3 * 256 * 256]
+    assert n1 == n0 + 2                                   # the two inputs' own passes
+    for p in (m.qkv.weight, m.proj.weight):
+        p.requires_grad_(False)
+    y2, codes, n2 = run(m, x)
+    assert codes == [3 * 256 * 256] and n2 == n0 and torch.equal(y2, y0)
+    y2.float().square().mean().backward()
+    assert m.q_norm.grad is not None and m.qkv.weight.grad is None
+    for p in m.parameters():
+        p.requires_grad_(False)
+    y3, codes, n3 = run(m, x)
+    assert codes == [] and n3 == n0 and torch.equal(y3, y0) and not y3.requires_grad
+
+
+def test_nothing_to_differentiate_writes_no_checkpoint():
+    """Rows and weights without gradients: the forward's pass is the one
+    without a checkpoint (its own kernel would store 1.03 bytes a value)."""
+    m = _module(checkpoint8=True)
+    for p in m.parameters():
+        p.requires_grad_(False)
+    x = torch.randn((256, 256), device="cuda").bfloat16()
+    made = []
+    empty = attention.Act8.empty
+    attention.Act8.empty = lambda *a, **kw: (made.append(a), empty(*a, **kw))[1]
+    try:
+        m(x)
+    finally:
+        attention.Act8.empty = empty
+    assert made == []

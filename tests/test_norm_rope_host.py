@@ -354,3 +354,20 @@ def test_linear8_takes_any_layout():
               torch.zeros((3, 2, 64)).transpose(0, 1), dense[0]):
         with pytest.raises(ValueError, match="x: expected a CUDA tensor"):
             Linear8Function.apply(x, w, None)
+
+
+def test_linear8_with_a_frozen_weight_stores_nothing():
+    """Without a gradient of the weight x is neither stored (which would need a
+    device) nor kept."""
+    from block_sparse_attention_layer_b200.attention import Linear8Function
+    w, b = torch.randn(8, 64), torch.randn(8, requires_grad=True)
+    for x in (torch.randn(6, 64), torch.randn(6, 64, requires_grad=True)):
+        kept = []
+        with torch.autograd.graph.saved_tensors_hooks(lambda t: (kept.append(t), t)[1], lambda t: t):
+            y = Linear8Function.apply(x, w, b)
+        assert [t.data_ptr() for t in kept] == ([w.data_ptr()] if x.requires_grad else [])
+        wanted = [t for t in (x, b) if t.requires_grad]
+        want = torch.autograd.grad(torch.nn.functional.linear(x, w, b).square().sum(), wanted)
+        got = torch.autograd.grad(y.square().sum(), wanted)
+        assert all(torch.equal(p, q) for p, q in zip(got, want))
+    assert not Linear8Function.apply(x.detach(), w, b.detach()).requires_grad
