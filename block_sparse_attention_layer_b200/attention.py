@@ -173,6 +173,18 @@ class Linear8Function(torch.autograd.Function):
         return dx, dw, db
 
 
+class Linear8(torch.nn.Linear):
+    """A linear layer that keeps its input for the weight's gradient in 8 bits
+    while ``checkpoint8`` is set."""
+
+    checkpoint8 = True
+
+    def forward(self, x):
+        if self.checkpoint8 and torch.is_grad_enabled():
+            return Linear8Function.apply(x, self.weight, self.bias)
+        return super().forward(x)
+
+
 class VMoBASelfAttention(torch.nn.Module):
     """Self-attention of one DiT layer over a (T, H, W) video latent with
     VMoBA in place of full attention.
@@ -190,7 +202,8 @@ class VMoBASelfAttention(torch.nn.Module):
     ``checkpoint8`` keeps what the backward needs of the activations in 8 bits:
     the projections' inputs and the raw q, k, v (5 bytes and 5 scales of a
     group for each token and channel in place of 10 in bf16).  Rotation and
-    checkpoints are part of the norm's pass, so both need ``qk_norm``.
+    checkpoints are part of the norm's pass, so both need ``qk_norm``.  A
+    module put in a projection's place keeps what it keeps itself.
     """
 
     def __init__(self, dim: int, n_heads: int, T: int, H: int, W: int, layer_idx: int,
@@ -205,14 +218,15 @@ class VMoBASelfAttention(torch.nn.Module):
         self.n_heads, self.head_dim = n_heads, dim // n_heads
         self.mode = _lib.mode_for_layer(layer_idx)
         self.tau = float(tau)
-        self.qkv = torch.nn.Linear(dim, 3 * dim, bias=True, device=device, dtype=dtype)
-        self.proj = torch.nn.Linear(dim, dim, bias=True, device=device, dtype=dtype)
+        linear = Linear8 if qk_norm else torch.nn.Linear
+        self.qkv = linear(dim, 3 * dim, bias=True, device=device, dtype=dtype)
+        self.proj = linear(dim, dim, bias=True, device=device, dtype=dtype)
         bt, bh, bw = boxes[self.mode]
         dt = "bf16" if dtype == torch.bfloat16 else "f32"
         self.shape = LayerShape(T, H, W, n_heads, self.head_dim, self.mode, bt, bh, bw, dt)
         self.layer = VMoBALayer(self.shape, device=device)
         self.scale = 1.0 / math.sqrt(self.head_dim)
-        self.norm_eps, self.checkpoint8 = float(norm_eps), bool(checkpoint8)
+        self.norm_eps, self.checkpoint8 = float(norm_eps), checkpoint8
         # like the layer's buffers, the rotation's table is the module's own: fp32
         # whatever type the parameters are moved to
         self.rope_dims, self.rope_table = (0, 0, 0), None
@@ -226,18 +240,26 @@ class VMoBASelfAttention(torch.nn.Module):
             self.rope_table = norm_rope.rope_table(self.shape, self.rope_dims, rope_base,
                                                    rope_origin, device)
 
+    @property
+    def checkpoint8(self) -> bool:
+        return self._checkpoint8
+
+    @checkpoint8.setter
+    def checkpoint8(self, on):
+        self._checkpoint8 = bool(on)
+        for m in (self.qkv, self.proj):
+            if isinstance(m, Linear8):
+                m.checkpoint8 = self._checkpoint8
+
     def forward(self, x: torch.Tensor, full_attention: bool = False) -> torch.Tensor:
         s = x.shape[0]
-        if self.q_norm is not None:
-            keep8 = self.checkpoint8 and torch.is_grad_enabled()
-            linear = Linear8Function.apply if keep8 else torch.nn.functional.linear
-            qkv = linear(x, self.qkv.weight, self.qkv.bias)
-            o = VMoBANormRopeFunction.apply(
-                qkv.view(s, 3, self.n_heads, self.head_dim), self.q_norm.float(),
-                self.k_norm.float(), self.layer, self.rope_table, self.rope_dims, self.norm_eps,
-                self.tau, bool(full_attention), self.scale, keep8)
-            return linear(o.view(s, -1), self.proj.weight, self.proj.bias)
         qkv = self.qkv(x).view(s, 3, self.n_heads, self.head_dim)
+        if self.q_norm is not None:
+            o = VMoBANormRopeFunction.apply(
+                qkv, self.q_norm.float(), self.k_norm.float(), self.layer, self.rope_table,
+                self.rope_dims, self.norm_eps, self.tau, bool(full_attention), self.scale,
+                self.checkpoint8 and torch.is_grad_enabled())
+            return self.proj(o.view(s, -1))
         q, k, v = (qkv[:, i].contiguous() for i in range(3))
         o = VMoBAFunction.apply(q, k, v, self.layer, self.tau, bool(full_attention), self.scale)
         return self.proj(o.reshape(s, self.n_heads * self.head_dim))

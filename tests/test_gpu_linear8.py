@@ -146,3 +146,54 @@ def test_nothing_to_differentiate_writes_no_checkpoint():
     finally:
         attention.Act8.empty = empty
     assert made == []
+
+
+class _Scaled(torch.nn.Module):
+    """A module put in a projection's place."""
+
+    def __init__(self, inner):
+        super().__init__()
+        self.inner = inner
+
+    @property
+    def weight(self):
+        return self.inner.weight
+
+    @property
+    def bias(self):
+        return self.inner.bias
+
+    def forward(self, x):
+        return 2 * self.inner(x)
+
+
+@pytest.mark.parametrize("ckpt", [False, True])
+def test_projections_are_called_as_modules(ckpt):
+    """Hooks on the projections run, modules put in their place are used, and
+    the switch can be set later."""
+    x = torch.randn((256, 256), device="cuda").bfloat16()
+    m = _module(checkpoint8=ckpt)
+    y0, seen = m(x), []
+    for name in ("qkv", "proj"):
+        getattr(m, name).register_forward_hook(lambda mod, i, o, name=name: seen.append(name))
+    doubled = m.proj.register_forward_hook(lambda mod, i, o: 2 * o)
+    y1 = m(x)
+    assert seen == ["qkv", "proj"] and torch.equal(y1, 2 * y0)
+    y1.float().square().mean().backward()
+    with torch.no_grad():
+        assert torch.equal(m(x), y1)
+    doubled.remove()
+    grads = {n: p.grad for n, p in m.named_parameters()}
+    other = _module(checkpoint8=ckpt)
+    other.proj = _Scaled(other.proj)
+    y2 = other(x)
+    assert torch.equal(y2, y1)
+    y2.float().square().mean().backward()
+    for n, p in other.named_parameters():
+        assert torch.equal(p.grad, grads[n.replace("proj.inner", "proj")])
+    late = _module(checkpoint8=not ckpt)
+    late.checkpoint8 = ckpt
+    assert late.checkpoint8 is ckpt
+    late.proj.register_forward_hook(lambda mod, i, o: 2 * o)
+    late(x).float().square().mean().backward()
+    assert all(torch.equal(p.grad, grads[n]) for n, p in late.named_parameters())
