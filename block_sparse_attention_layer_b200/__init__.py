@@ -15,27 +15,16 @@ from ._lib import (  # noqa: F401
     score_select_variant, SELECT_VARIANTS, HEAD_STATS_DTYPE,
 )
 
-# norm + rotation and 8-bit checkpoints (norm_rope.py), loaded when first used:
-# that module needs torch, which the rest imports only where it must
-_NORM_ROPE = (
-    "NormRope", "Act8", "rope_dims", "rope_table", "qk_norm_rope", "qk_norm_rope_partition",
-    "qk_norm_rope_bwd", "qk_norm_rope_bwd_workspace_size", "act8_pack", "act8_unpack",
+from .norm_rope import (  # noqa: F401
+    NormRope, Act8, rope_dims, rope_table, qk_norm_rope, qk_norm_rope_partition, qk_norm_rope_bwd,
+    qk_norm_rope_bwd_workspace_size, act8_pack, act8_unpack,
 )
-
-
-def __getattr__(name):
-    if name in _NORM_ROPE:
-        from . import norm_rope
-        for n in _NORM_ROPE:
-            globals()[n] = getattr(norm_rope, n)
-        return globals()[name]
-    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
-
 
 __all__ = [
     "LayerShape", "VmobaError", "lib", "mode_for_layer", "num_blocks", "workspace_size",
     "bwd_workspace_size", "partition", "score_select", "build_plan", "attn_fwd", "attn_bwd",
     "get_status", "decode_stats", "default_scale", "kernel_launches", "trace_enable", "trace_read",
     "score_select_static", "score_select_variant", "SELECT_VARIANTS", "HEAD_STATS_DTYPE",
-    *_NORM_ROPE,
+    "NormRope", "Act8", "rope_dims", "rope_table", "qk_norm_rope", "qk_norm_rope_partition",
+    "qk_norm_rope_bwd", "qk_norm_rope_bwd_workspace_size", "act8_pack", "act8_unpack",
 ]

@@ -5,7 +5,8 @@ checkpoints in 8 bits (include/vmoba.h: vmoba_norm_rope, vmoba_act8_pack).
 Binding only, as _lib: arguments are checked and passed on, every step runs in
 libvmoba's kernels on the caller's buffers.  The checks are native
 (csrc/calls.cpp) and raise ValueError; a call's tensors lie on one CUDA device,
-which is made current during the call.
+which is made current during the call.  Importing loads neither the library nor
+the native calls; the first call does, and raises if they are missing.
 """
 from __future__ import annotations
 
@@ -13,17 +14,8 @@ import ctypes
 import os
 from dataclasses import dataclass
 
-import torch
-
 from . import _lib
 from ._lib import LayerShape
-
-if not os.path.exists(os.path.join(os.path.dirname(__file__), "_calls.so")):
-    raise RuntimeError("_calls.so is missing: build it with "
-                       "`python -m block_sparse_attention_layer_b200.build`")
-from . import _calls  # noqa: E402
-
-_F32, _I8 = torch.float32, torch.int8
 
 
 @dataclass(frozen=True, eq=False)
@@ -49,12 +41,13 @@ class Act8:
 
     @classmethod
     def empty(cls, shape, group: int, device="cuda") -> "Act8":
+        import torch
         if group not in (64, 128):
             raise ValueError("group: expected 64 or 128")
         shape = tuple(shape)
         n = -(-shape[-1] // group)
-        return cls(torch.empty(shape, dtype=_I8, device=device),
-                   torch.empty(shape[:-1] + (n,), dtype=_F32, device=device), group)
+        return cls(torch.empty(shape, dtype=torch.int8, device=device),
+                   torch.empty(shape[:-1] + (n,), dtype=torch.float32, device=device), group)
 
 
 def rope_dims(head_dim: int) -> tuple:
@@ -67,14 +60,20 @@ def rope_dims(head_dim: int) -> tuple:
 _ENTRIES = ("vmoba_qk_norm_rope", "vmoba_qk_norm_rope_act8", "vmoba_qk_norm_rope_partition",
             "vmoba_qk_norm_rope_partition_act8", "vmoba_qk_norm_rope_bwd",
             "vmoba_qk_norm_rope_bwd_act8", "vmoba_act8_pack", "vmoba_act8_unpack")
-_bound = False
+_calls, _bound = None, False
 
 
 def _bind() -> None:
-    """Hand the library's entries to the native calls (at the first one)."""
-    global _bound
-    L = _lib.lib()
-    _calls.bind({n: ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in _ENTRIES}, Act8)
+    """Load the native calls and hand them the library's entries (at the first one)."""
+    global _calls, _bound
+    if not os.path.exists(os.path.join(os.path.dirname(__file__), "_calls.so")):
+        raise RuntimeError("_calls.so is missing: build it with "
+                           "`python -m block_sparse_attention_layer_b200.build`")
+    import torch  # noqa: F401  (whose libraries the native calls link against)
+
+    from . import _calls as native
+    _calls, L = native, _lib.lib()
+    native.bind({n: ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in _ENTRIES}, Act8)
     _bound = True
 
 
@@ -83,11 +82,12 @@ def rope_table(shape: LayerShape, dims, base: float = 10000.0, origin=(0, 0, 0),
     """The rotation table of the shape's grid: (cos, sin) of each position and
     pair of the three axes, [T dims[0]/2 + H dims[1]/2 + W dims[2]/2][2] fp32,
     positions counted from ``origin`` (a chunk of a longer video)."""
+    import torch
     t, h, w = (int(n) for n in dims)
     if min(t, h, w) < 0 or (t | h | w) & 1 or t + h + w > shape.head_dim:
         raise ValueError(f"dims: expected three even numbers >= 0 of sum <= {shape.head_dim}, "
                          f"got {dims}")
-    table = torch.empty(((shape.T * t + shape.H * h + shape.W * w) // 2, 2), dtype=_F32,
+    table = torch.empty(((shape.T * t + shape.H * h + shape.W * w) // 2, 2), dtype=torch.float32,
                         device=device)
     if not table.is_cuda:
         raise ValueError("device: expected a CUDA device")
@@ -104,7 +104,8 @@ def qk_norm_rope(shape, nr, qkv, q, k, v, ckpt=None, stream=None) -> None:
     [s][3][heads][d] (tokens any stride apart), three [s][heads][d] tensors, or
     an Act8 checkpoint of it; ckpt: an Act8 to store the raw rows in (groups
     of head_dim), in the same pass."""
-    rc = _calls.forward(shape._native, nr, qkv, q, k, v, None, ckpt, stream)
+    native = shape._native
+    rc = _calls.forward(native, nr, qkv, q, k, v, None, ckpt, stream)
     if rc:
         _lib._check("vmoba_qk_norm_rope", rc)
 
@@ -116,7 +117,8 @@ def qk_norm_rope_partition(shape, nr, qkv, q, k_perm, v_perm, blocks, ckpt=None,
     fp32 means ``blocks`` of the rotated keys (before rounding to storage)."""
     if blocks is None:
         raise ValueError("blocks: expected a tensor")
-    rc = _calls.forward(shape._native, nr, qkv, q, k_perm, v_perm, blocks, ckpt, stream)
+    native = shape._native
+    rc = _calls.forward(native, nr, qkv, q, k_perm, v_perm, blocks, ckpt, stream)
     if rc:
         _lib._check("vmoba_qk_norm_rope_partition", rc)
 
@@ -130,7 +132,8 @@ def qk_norm_rope_bwd(shape, nr, qkv, dq, dk, dv, dqkv, dweight, ws, stream=None)
     (token order) -> of the raw rows (dqkv, laid out like qkv) and of the two
     norm weights (dweight [2][d] fp32, or None: then ws may be None too).  qkv:
     the forward's raw rows or their Act8 checkpoint."""
-    rc = _calls.backward(shape._native, nr, qkv, dq, dk, dv, dqkv, dweight, ws, stream)
+    native = shape._native
+    rc = _calls.backward(native, nr, qkv, dq, dk, dv, dqkv, dweight, ws, stream)
     if rc:
         _lib._check("vmoba_qk_norm_rope_bwd", rc)
 

@@ -371,3 +371,47 @@ def test_linear8_with_a_frozen_weight_stores_nothing():
         got = torch.autograd.grad(y.square().sum(), wanted)
         assert all(torch.equal(p, q) for p, q in zip(got, want))
     assert not Linear8Function.apply(x.detach(), w, b.detach()).requires_grad
+
+
+_WITHOUT = """
+import importlib.abc, sys
+class Blocked(importlib.abc.MetaPathFinder):
+    def find_spec(self, name, path=None, target=None):
+        if name.split('.')[-1].startswith('_calls') or name == BLOCK:
+            raise ImportError(name + ' is blocked')
+sys.meta_path.insert(0, Blocked())
+"""
+
+
+def _python(code):
+    return subprocess.run([sys.executable, "-c", code], timeout=100, text=True, capture_output=True,
+                          cwd=os.path.dirname(os.path.dirname(__file__)))
+
+
+def test_the_plain_layer_imports_without_the_native_calls():
+    """The attention, its module and the names of the package load without
+    _calls; the first call of what needs it raises."""
+    done = _python("BLOCK = None" + _WITHOUT + """
+import block_sparse_attention_layer_b200 as V
+from block_sparse_attention_layer_b200 import attention, layer, norm_rope
+from block_sparse_attention_layer_b200 import *
+import torch
+c, x = V.Act8.empty((4, 64), 64, 'cpu'), torch.zeros(4, 64)
+sh = V.LayerShape(4, 8, 8, 2, 64, 2, 2, 4, 4, 'bf16')
+for call in (lambda: V.act8_pack(x, c), lambda: V.act8_unpack(c, x),
+             lambda: V.qk_norm_rope(sh, V.NormRope(), x, x, x, x)):
+    try:
+        call()
+    except (ImportError, RuntimeError) as e:
+        assert '_calls' in str(e)
+        print('raised')
+""")
+    assert done.stdout.split() == ["raised"] * 3, done.stderr
+
+
+def test_the_package_names_load_without_torch():
+    done = _python("BLOCK = 'torch'" + _WITHOUT + """
+from block_sparse_attention_layer_b200 import *
+print(lib() is not None, rope_dims(128) == (44, 42, 42), 'torch' in sys.modules)
+""")
+    assert done.stdout.split() == ["True", "True", "False"], done.stderr
