@@ -415,3 +415,43 @@ from block_sparse_attention_layer_b200 import *
 print(lib() is not None, rope_dims(128) == (44, 42, 42), 'torch' in sys.modules)
 """)
     assert done.stdout.split() == ["True", "True", "False"], done.stderr
+
+
+@pytest.fixture
+def fake_tools(tmp_path, monkeypatch):
+    """The build script with its outputs in a folder of its own and compilers
+    that only make their output file; the list of what they were asked for."""
+    from block_sparse_attention_layer_b200 import build as B
+    ran, broken = [], []
+
+    def run(cmd, **kw):
+        out = os.path.basename(cmd[cmd.index("-o") + 1])
+        ran.append(out)
+        if any(out.startswith(b) for b in broken):
+            return subprocess.CompletedProcess(cmd, 1, "", "no such header")
+        open(cmd[cmd.index("-o") + 1], "w").close()
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+
+    monkeypatch.setattr(B.subprocess, "run", run)
+    monkeypatch.setattr(B, "nvcc", lambda: "/usr/local/cuda/bin/nvcc")
+    for name in ("LIB", "OBJ", "CALLS", "PKG"):
+        if hasattr(B, name):
+            monkeypatch.setattr(B, name, str(tmp_path / os.path.basename(getattr(B, name))))
+    os.makedirs(B.PKG, exist_ok=True)
+    return B, ran, broken
+
+
+def test_the_library_builds_without_the_native_calls(fake_tools):
+    """Where the Python calls cannot be compiled the library is there all the
+    same, and the reason is told."""
+    B, ran, broken = fake_tools
+    broken.append("_calls")
+    with pytest.warns(RuntimeWarning, match="no such header"):
+        assert B.build(jobs=1) == B.LIB
+    assert os.path.exists(B.LIB) and ran[-1].startswith("_calls")
+    broken.clear()
+    ran.clear()
+    B.build(jobs=1)
+    assert len(ran) == 1 and ran[0].startswith("_calls")
+    B.build(jobs=1)
+    assert len(ran) == 1
