@@ -6,9 +6,10 @@ Every .cu file under csrc/ is compiled for sm_100a only
 (-gencode arch=compute_100a,code=sm_100a) with -lineinfo and linked into
 block_sparse_attention_layer_b200/libvmoba.so against the static CUDA
 runtime; csrc/calls.cpp, the Python calls of norm_rope.py, is then compiled
-against torch's headers into _calls.so beside it (where that cannot be done a
-warning says why, and only norm_rope's calls are missing).  Rebuilds only when
-a source or header is newer than what was built from it.
+against torch's headers into _calls.torch-<version>....so beside it, one for
+each torch and Python (where that cannot be done a warning says why, and only
+norm_rope's calls are missing).  Rebuilds only when a source or header is newer
+than what was built from it.
 """
 from __future__ import annotations
 
@@ -26,7 +27,6 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libvmoba.so")
-CALLS = os.path.join(PKG, "_calls.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O3",
@@ -69,15 +69,26 @@ def _compile(src: str, verbose_ptxas: bool) -> str:
     return obj
 
 
+def calls_path() -> str:
+    """The native Python calls (csrc/calls.cpp) of this interpreter and torch,
+    both of which fix their binary interface."""
+    import sysconfig
+
+    import torch
+    return os.path.join(PKG, f"_calls.torch-{torch.__version__}-{int(torch.compiled_with_cxx11_abi())}"
+                             f"{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
 def build_calls(force: bool = False) -> str:
     """Compile csrc/calls.cpp against the installed torch."""
+    calls = calls_path()
     src = os.path.join(CSRC, "calls.cpp")
     deps = [src, *glob.glob(os.path.join(ROOT, "include", "*.h"))]
-    if not force and os.path.exists(CALLS) and \
-            all(os.path.getmtime(p) <= os.path.getmtime(CALLS) for p in deps):
-        return CALLS
-    if os.path.exists(CALLS):
-        os.remove(CALLS)                # of an older source: must not be taken for this one's
+    if not force and os.path.exists(calls) and \
+            all(os.path.getmtime(p) <= os.path.getmtime(calls) for p in deps):
+        return calls
+    if os.path.exists(calls):
+        os.remove(calls)                # of an older source: must not be taken for this one's
     import sysconfig
 
     import torch
@@ -88,13 +99,13 @@ def build_calls(force: bool = False) -> str:
     cxx = os.environ.get("CXX") or shutil.which("g++") or "c++"
     cmd = [cxx, "-O2", "-std=c++17", "-shared", "-fPIC", *("-I" + i for i in include),
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", src,
-           "-o", CALLS + ".tmp", "-L" + os.path.join(root, "lib"),
+           "-o", calls + ".tmp", "-L" + os.path.join(root, "lib"),
            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"{cxx} failed for {src}:\n{r.stderr}")
-    os.replace(CALLS + ".tmp", CALLS)
-    return CALLS
+    os.replace(calls + ".tmp", calls)
+    return calls
 
 
 def build(force: bool = False, jobs: int = 0, verbose_ptxas: bool = False) -> str:

@@ -11,6 +11,8 @@ the native calls; the first call does, and raises if they are missing.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 from dataclasses import dataclass
 
@@ -66,12 +68,15 @@ _calls, _bound = None, False
 def _bind() -> None:
     """Load the native calls and hand them the library's entries (at the first one)."""
     global _calls, _bound
-    if not os.path.exists(os.path.join(os.path.dirname(__file__), "_calls.so")):
-        raise RuntimeError("_calls.so is missing: build it with "
+    from .build import calls_path
+    path = calls_path()
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is missing: build it with "
                            "`python -m block_sparse_attention_layer_b200.build`")
-    import torch  # noqa: F401  (whose libraries the native calls link against)
-
-    from . import _calls as native
+    loader = importlib.machinery.ExtensionFileLoader(__package__ + "._calls", path)
+    spec = importlib.util.spec_from_file_location(loader.name, path, loader=loader)
+    native = importlib.util.module_from_spec(spec)
+    loader.exec_module(native)
     _calls, L = native, _lib.lib()
     native.bind({n: ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in _ENTRIES}, Act8)
     _bound = True

@@ -380,6 +380,9 @@ class Blocked(importlib.abc.MetaPathFinder):
         if name.split('.')[-1].startswith('_calls') or name == BLOCK:
             raise ImportError(name + ' is blocked')
 sys.meta_path.insert(0, Blocked())
+import os.path
+exists = os.path.exists
+os.path.exists = lambda p: '_calls' not in str(p) and exists(p)
 """
 
 
@@ -455,3 +458,18 @@ def test_the_library_builds_without_the_native_calls(fake_tools):
     assert len(ran) == 1 and ran[0].startswith("_calls")
     B.build(jobs=1)
     assert len(ran) == 1
+
+
+def test_native_calls_belong_to_one_torch(fake_tools, monkeypatch):
+    """What was built against another torch is neither current nor loaded."""
+    B, ran, _ = fake_tools
+    B.build(jobs=1)
+    assert len([r for r in ran if r.startswith("_calls")]) == 1
+    monkeypatch.setattr(torch, "__version__", "0.0.1")
+    with monkeypatch.context() as m:
+        from block_sparse_attention_layer_b200 import norm_rope
+        m.setattr(norm_rope, "_bound", False)
+        with pytest.raises(RuntimeError, match="missing: build it"):
+            norm_rope._bind()
+    B.build(jobs=1)
+    assert len([r for r in ran if r.startswith("_calls")]) == 2
