@@ -40,12 +40,12 @@ class VMoBAFunction(torch.autograd.Function):
 
     The backward kernels read state the forward left in the layer's buffers
     (permuted keys and values, pair lists, LSE, the fp32 output copy).  Each
-    call keeps its own selection bitmap and records the layer's forward
-    generation; if another forward ran on the same layer in between (two
-    micro-batches, activation checkpointing, a full-attention call), the
-    backward first restores this call's state by re-running partition, plan
-    and forward on its saved inputs and selection -- the same deterministic
-    kernels, so the restored state is bit-identical -- and then runs.
+    call keeps its own selection bitmap and records the layer's generation; if
+    another call wrote to that state in between (two micro-batches, activation
+    checkpointing, a full-attention call, another selection), the backward
+    first restores this call's state by re-running partition, plan and forward
+    on its saved inputs and selection -- the same deterministic kernels, so the
+    restored state is bit-identical -- and then runs.
     """
 
     @staticmethod
@@ -66,7 +66,7 @@ class VMoBAFunction(torch.autograd.Function):
         q, k, v, sel = ctx.saved_tensors
         layer = ctx.layer
         if layer.generation != ctx.generation:
-            # another forward replaced this call's state: rebuild it
+            # another call replaced a part of this one's state: rebuild it
             layer.partition_only(k, v)
             layer.use_selection(sel)
             layer.forward(q, ctx.scale)
@@ -82,10 +82,10 @@ class VMoBANormRopeFunction(torch.autograd.Function):
 
     Saved for the backward are the raw rows, or with ``checkpoint8`` their
     8-bit checkpoint (written by the forward's own pass), and the selection.
-    The other state stays in the layer's buffers; if another forward ran on
-    the layer in between, the backward rebuilds it from what was saved: from
-    the raw rows bit for bit, from a checkpoint as the attention of the values
-    it holds.  The gradients of the raw rows and norm weights are taken at the
+    The other state stays in the layer's buffers; if another call wrote to it
+    in between, the backward rebuilds it from what was saved: from the raw
+    rows bit for bit, from a checkpoint as the attention of the values it
+    holds.  The gradients of the raw rows and norm weights are taken at the
     saved values in either case.
     """
 
@@ -118,7 +118,7 @@ class VMoBANormRopeFunction(torch.autograd.Function):
         norm = NormRope(q_weight, k_weight, ctx.eps, table, ctx.dims)
         raw = Act8(*saved, layer.shape.head_dim) if ctx.has[3] else saved[0]
         if layer.generation != ctx.generation:
-            # another forward replaced this call's state: rebuild it
+            # another call replaced a part of this one's state: rebuild it
             layer.prologue(raw, norm)
             layer.use_selection(sel)
             layer.forward(layer.q, ctx.scale)

@@ -45,9 +45,9 @@ class VMoBALayer:
         self.dq = torch.empty((s, h, d), dtype=dt, device=dev)
         self.dk = torch.empty((s, h, d), dtype=dt, device=dev)
         self.dv = torch.empty((s, h, d), dtype=dt, device=dev)
-        # forwards (and prologues) run so far: lets a caller tell whether the
-        # forward state in the buffers (LSE, fp32 output copy, pair lists) is
-        # still its own
+        # calls so far that wrote a part of the forward state in the buffers
+        # (permuted keys and values, selection, pair lists, LSE, fp32 output
+        # copy): lets a caller tell whether that state is still its own
         self.generation = 0
         self._device = dev
 
@@ -70,7 +70,7 @@ class VMoBALayer:
         self.k_perm, self.v_perm and self.blocks: norm, rotation, partition
         and pooling in one pass (norm_rope.qk_norm_rope_partition); ckpt: an
         Act8 to store the raw rows in.  The state of an earlier forward ends
-        here (as a forward does, this counts as a new generation)."""
+        here, as with every call that writes a part of it (generation)."""
         self.generation += 1
         norm_rope.qk_norm_rope_partition(self.shape, norm, qkv, self.q, self.k_perm, self.v_perm,
                                          self.blocks, ckpt=ckpt)
@@ -78,6 +78,7 @@ class VMoBALayer:
     def select_pooled(self, q, tau, scale=0.0):
         """Selection and plan from the block means already in self.blocks."""
         sh = self.shape
+        self.generation += 1
         _lib.score_select(sh, q, self.blocks, tau, scale, self.sel, self.stats, self.ws)
         _lib.build_plan(sh, self.sel, self.ws)
 
@@ -91,6 +92,7 @@ class VMoBALayer:
 
     def select(self, q, k, v, tau, scale=0.0):
         sh = self.shape
+        self.generation += 1
         _lib.partition(sh, k, v, self.k_perm, self.v_perm, self.blocks)
         _lib.score_select(sh, q, self.blocks, tau, scale, self.sel, self.stats, self.ws)
         _lib.build_plan(sh, self.sel, self.ws)
@@ -100,6 +102,7 @@ class VMoBALayer:
         _lib.score_select_variant): "threshold_global" (the method),
         "topk_global", "threshold_local", "topk_local"."""
         sh = self.shape
+        self.generation += 1
         _lib.partition(sh, k, v, self.k_perm, self.v_perm, self.blocks)
         _lib.score_select_variant(sh, q, self.blocks, variant, param, scale, self.sel,
                                   self.stats, self.ws)
@@ -107,16 +110,18 @@ class VMoBALayer:
 
     def use_selection(self, sel_bits):
         """Adopt a caller-built bitmap (e.g. a reference selection) and plan for it."""
+        self.generation += 1
         self.sel.copy_(sel_bits)
         _lib.build_plan(self.shape, self.sel, self.ws)
 
     def partition_only(self, k, v):
+        self.generation += 1
         _lib.partition(self.shape, k, v, self.k_perm, self.v_perm, self.blocks)
 
     def forward(self, q, scale=0.0):
+        self.generation += 1
         _lib.attn_fwd(self.shape, q, self.k_perm, self.v_perm, self.sel, self.ws, scale,
                       self.out, self.lse)
-        self.generation += 1
         return self.out, self.lse
 
     def backward(self, q, dout, scale=0.0):

@@ -297,3 +297,21 @@ def test_forward_and_backward_in_a_graph():
         eager = step()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(kept, eager))
+
+
+@pytest.mark.parametrize("between", ["select_pooled", "select", "select_variant", "use_selection",
+                                     "partition_only"])
+def test_a_selection_in_between_ends_the_state(between):
+    """A selection or partition on the layer between forward and backward, with
+    no forward after it: the gradients are still the first call's."""
+    table, layer = _table(), _layer()
+    qkv, gq, gk, dout = _inputs(47)
+    out = _apply(layer, qkv, gq, gk, table)
+    a, b, c = (t.contiguous() for t in _inputs(48, leaf=False)[0].unbind(1))
+    args = dict(select_pooled=(layer.q, 0.1, SCALE), select=(a, b, c, 0.1, SCALE),
+                select_variant=(a, b, c, "topk_global", 100, SCALE),
+                use_selection=(torch.zeros_like(layer.sel),), partition_only=(b, c))[between]
+    getattr(layer, between)(*args)
+    out.backward(dout)
+    _, dqkv, dw = _by_hand(_layer(), qkv.detach(), gq.detach(), gk.detach(), dout, table)
+    assert torch.equal(qkv.grad, dqkv) and torch.equal(gq.grad, dw[0])

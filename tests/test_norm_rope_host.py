@@ -473,3 +473,21 @@ def test_native_calls_belong_to_one_torch(fake_tools, monkeypatch):
             norm_rope._bind()
     B.build(jobs=1)
     assert len([r for r in ran if r.startswith("_calls")]) == 2
+
+
+@pytest.mark.parametrize("call", ["prologue", "select_pooled", "select", "select_variant",
+                                  "use_selection", "partition_only", "forward"])
+def test_every_call_that_changes_the_state_counts(call, monkeypatch):
+    """The forward state of a layer (keys, selection, plan, LSE) ends with any
+    call that writes a part of it; a backward tells so by the generation."""
+    from block_sparse_attention_layer_b200 import layer as lay
+    for name in ("partition", "score_select", "score_select_variant", "build_plan", "attn_fwd"):
+        monkeypatch.setattr(_lib, name, lambda *a, **kw: None)
+    monkeypatch.setattr(lay.norm_rope, "qk_norm_rope_partition", lambda *a, **kw: None)
+    layer = lay.VMoBALayer(_shape(), device="cpu", max_pair_fraction=0.1)
+    t, before = torch.zeros(1), layer.generation
+    args = dict(prologue=(t, None), select_pooled=(t, 0.3), select=(t, t, t, 0.3),
+                select_variant=(t, t, t, "topk_global", 2), use_selection=(layer.sel.clone(),),
+                partition_only=(t, t), forward=(t,))[call]
+    getattr(layer, call)(*args)
+    assert layer.generation > before
