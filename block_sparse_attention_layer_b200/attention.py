@@ -204,12 +204,19 @@ class VMoBASelfAttention(torch.nn.Module):
     group for each token and channel in place of 10 in bf16).  Rotation and
     checkpoints are part of the norm's pass, so both need ``qk_norm``.  A
     module put in a projection's place keeps what it keeps itself.
+
+    ``layer`` shares another module's buffers (``other.layer``, of the same
+    latent, heads, boxes and mode), which are far more than an activation: 14
+    bytes a token and channel in bf16, and the workspace.  Every module but
+    the last to run forward then rebuilds its state in the backward (one more
+    attention forward).
     """
 
     def __init__(self, dim: int, n_heads: int, T: int, H: int, W: int, layer_idx: int,
                  boxes, tau: float = 0.25, dtype=torch.bfloat16, device="cuda", *,
                  qk_norm: bool = False, norm_eps: float = 1e-6, rope=None,
-                 rope_base: float = 10000.0, rope_origin=(0, 0, 0), checkpoint8: bool = False):
+                 rope_base: float = 10000.0, rope_origin=(0, 0, 0), checkpoint8: bool = False,
+                 layer: VMoBALayer | None = None):
         super().__init__()
         if not qk_norm and (rope or checkpoint8):
             raise ValueError("rope and checkpoint8 need qk_norm")
@@ -224,7 +231,9 @@ class VMoBASelfAttention(torch.nn.Module):
         bt, bh, bw = boxes[self.mode]
         dt = "bf16" if dtype == torch.bfloat16 else "f32"
         self.shape = LayerShape(T, H, W, n_heads, self.head_dim, self.mode, bt, bh, bw, dt)
-        self.layer = VMoBALayer(self.shape, device=device)
+        if layer is not None and layer.shape != self.shape:
+            raise ValueError(f"layer: expected one of shape {self.shape}, got {layer.shape}")
+        self.layer = VMoBALayer(self.shape, device=device) if layer is None else layer
         self.scale = 1.0 / math.sqrt(self.head_dim)
         self.norm_eps, self.checkpoint8 = float(norm_eps), checkpoint8
         # like the layer's buffers, the rotation's table is the module's own: fp32

@@ -197,3 +197,31 @@ def test_projections_are_called_as_modules(ckpt):
     late.proj.register_forward_hook(lambda mod, i, o: 2 * o)
     late(x).float().square().mean().backward()
     assert all(torch.equal(p.grad, grads[n]) for n, p in late.named_parameters())
+
+
+@pytest.mark.parametrize("ckpt", [False, True])
+def test_modules_share_one_layer(ckpt):
+    """Two modules on one layer's buffers: the outputs of modules with their
+    own, and their gradients too (from a checkpoint for the second one only:
+    the first one's attention is then rebuilt from the stored values)."""
+    x = torch.randn((256, 256), device="cuda").bfloat16()
+    own = [_module(checkpoint8=ckpt), _module(checkpoint8=ckpt)]
+    shared = [_module(checkpoint8=ckpt)]
+    shared.append(_module(checkpoint8=ckpt, layer=shared[0].layer))
+    assert shared[1].layer is shared[0].layer
+    for m in (own[1], shared[1]):
+        with torch.no_grad():
+            m.proj.bias.add_(1.0)
+    ys = [m[1](m[0](x)) for m in (own, shared)]
+    assert torch.equal(*ys)
+    for y in ys:
+        y.float().square().mean().backward()
+    for i in ((1,) if ckpt else (0, 1)):
+        for (n, p), q in zip(own[i].named_parameters(), shared[i].parameters()):
+            assert torch.equal(p.grad, q.grad), n
+    # rebuilt from stored values: there and finite
+    for p, q in zip(own[0].parameters(), shared[0].parameters()):
+        assert torch.isfinite(q.grad).all() and p.grad.abs().max() > 0
+    other = V.LayerShape(4, 8, 8, 2, 128, 1, 4, 4, 4, "bf16")
+    with pytest.raises(ValueError, match="layer: expected one of shape"):
+        _module(layer=attention.VMoBALayer(other))
