@@ -8,6 +8,7 @@ import pytest
 
 import oracle as O
 
+from . import norm_rope_attn_ref as A
 from . import norm_rope_ref as R
 from .gpu_util import TOL, from_device, out_err, unpack_bits
 
@@ -315,3 +316,56 @@ def test_a_selection_in_between_ends_the_state(between):
     out.backward(dout)
     _, dqkv, dw = _by_hand(_layer(), qkv.detach(), gq.detach(), gk.detach(), dout, table)
     assert torch.equal(qkv.grad, dqkv) and torch.equal(gq.grad, dw[0])
+
+
+@pytest.mark.parametrize("mode,full", [(0, False), (1, False), (2, False), (2, True)])
+def test_gradients_of_the_run_within_their_own_bounds(mode, full):
+    """The two halves of the backward, each against its own formula: the
+    attention's dq and dk against the oracle's at the rows that the forward
+    made, within the bound of their fp16 operands; then the raw rows' and the
+    norm weights' gradients against the plain norm backward of those very dq
+    and dk, within the norm's own fp32 bounds.  Gradients that are zero,
+    negated or a tenth off are outside of either."""
+    layer, table = _layer(mode), _table()
+    qkv, gq, gk, dout = _inputs(70 + mode)
+    _apply(layer, qkv, gq, gk, table, full=full).backward(dout)
+    torch.cuda.synchronize()
+    z = R.phases(T, H, W, D, DIMS, table.double().cpu().numpy())
+    box = O.mode_box(mode, T, H, W, *BOXES[mode])
+    order = O.partition_order(T, H, W, box)
+    back = np.empty_like(order)
+    back[order] = np.arange(S)
+    q = from_device(layer.q)
+    k, v = (from_device(t).transpose(1, 0, 2)[back] for t in (layer.k_perm, layer.v_perm))
+    sel, blk = unpack_bits(layer.sel.cpu().numpy(), layer.n_blocks), O.block_of_token(T, H, W, box)
+    dy = dout.double().cpu().numpy()
+    lse = O.attention_fwd(q, k, v, sel, blk, SCALE)[1]
+    some = sel.any(-1)
+    assert (np.abs(layer.lse.double().cpu().numpy()[some] - lse[some]) <= A.LSE).all()
+    ref = O.attention_bwd(q, k, v, sel, blk, SCALE, dy)
+    bounds = A.attention_bounds(q, k, v, sel[:, :, blk], SCALE, dy)
+
+    def within(got, want, bound):
+        return np.abs(got - want) <= bound + R.STEP["bf16"] * (np.abs(want) + bound) + \
+            R.TINY["bf16"]
+
+    def rejects(check, got):
+        return not check(0 * got).all() and not check(-got).all() and not check(1.1 * got).all()
+
+    grads = [from_device(layer.dq), from_device(layer.dk)]
+    for i in range(2):
+        check = lambda g: within(g, ref[i], bounds[i])                  # noqa: E731
+        assert check(grads[i]).all()
+        assert rejects(check, grads[i]) and check(0 * grads[i]).mean() < 0.5
+    raw = qkv.detach().double().cpu().numpy()
+    got = qkv.grad.double().cpu().numpy()
+    for i, g in enumerate((gq, gk)):
+        dx, b, dg, bg = R.backward(raw[:, i], g.detach().double().cpu().numpy(), EPS, z, grads[i])
+        check = lambda x: within(x, dx, b)                              # noqa: E731
+        assert check(got[:, i]).all()
+        assert rejects(check, got[:, i]) and check(0 * dx).mean() < 0.5     # rows without a pair are zero
+        check = lambda w: np.abs(w - dg) <= bg + R.U * np.abs(dg)       # noqa: E731
+        dgot = g.grad.double().cpu().numpy()
+        assert check(dgot).all()
+        assert rejects(check, dgot) and check(0 * dgot).mean() < 0.05
+    assert np.array_equal(got[:, 2], from_device(layer.dv))
