@@ -189,3 +189,54 @@ def test_widest_rows(cols, group):
         assert np.array_equal(ckpt.scales[:, -1:].cpu().numpy(), scales)
         back = torch.from_numpy(R.decode8(codes, scales, group)).to(out.dtype)
         assert torch.equal(out[:, whole:].cpu(), back)
+
+
+def _bf16_pairs():
+    """(values [n][64] bf16, codes) of groups whose largest value has each of
+    the 128 bf16 significands, at some exponents, and whose others run over
+    every significand at every exponent down to a code of zero, both signs:
+    the code is round-half-even of 127 x / a, in whole numbers."""
+    m = np.arange(128, 256)
+    x, e = np.meshgrid(m, np.arange(10), indexing="ij")
+    x, e = (np.concatenate((t.ravel(), t.ravel())) for t in (x, e))
+    sign = np.where(np.arange(x.size) < x.size // 2, 1, -1)
+    groups, codes = [], []
+    for a in m:
+        keep = (x <= a) | (e > 0)                        # |x| <= a 2^e / 2^e
+        num, den = 127 * x[keep], a << e[keep]           # 127 |x| / a, exactly
+        c, rest = num // den, 2 * (num % den)
+        c = c + ((rest > den) | ((rest == den) & (c % 2 == 1)))
+        v, c = sign[keep] * x[keep] * 2.0 ** -e[keep], sign[keep] * c
+        pad = -v.size % 63
+        v, c = np.pad(v, (0, pad)).reshape(-1, 63), np.pad(c, (0, pad)).reshape(-1, 63)
+        groups.append(np.insert(v, 0, a, 1))
+        codes.append(np.insert(c, 0, 127, 1))
+    return np.concatenate(groups), np.concatenate(codes)
+
+
+def test_every_pair_of_bf16_significands():
+    """The one rounding that a bf16 group's codes go through is the exact
+    quotient's, for every value against every largest one."""
+    values, codes = _bf16_pairs()
+    for shift in (-100, -7, 0, 60, 92, 110):
+        x = torch.from_numpy(values * 2.0 ** shift).to(torch.bfloat16)
+        assert torch.equal(x.double(), torch.from_numpy(values * 2.0 ** shift))
+        ckpt = V.Act8.empty(tuple(x.shape), 64)
+        V.act8_pack(x.cuda(), ckpt)
+        assert np.array_equal(ckpt.codes.cpu().numpy(), codes)
+
+
+def test_every_fp32_scale():
+    """a / 127 is correctly rounded for every significand of a: the host's
+    division is, and no exponent changes it while the results are normal."""
+    for shift in (-110, 0, 100):
+        for first in range(1 << 23, 1 << 24, 1 << 21):
+            a = torch.arange(first, first + (1 << 21), dtype=torch.float64) * 2.0 ** (shift - 23)
+            a = a.float()
+            x = torch.zeros((a.numel(), 64), device="cuda")
+            x[:, 5] = -a.cuda()
+            ckpt = V.Act8.empty(tuple(x.shape), 64)
+            V.act8_pack(x, ckpt)
+            want = torch.from_numpy(a.numpy() / np.float32(127.0))
+            assert torch.equal(ckpt.scales[:, 0].cpu(), want)
+            assert (ckpt.codes[:, 5] == -127).all()
