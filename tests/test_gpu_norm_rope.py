@@ -524,3 +524,56 @@ def test_weights_made_at_each_access_live_through_the_call():
     V.qk_norm_rope_bwd(c.sh, Norm(), c.qkv, *c.grads, raw, got, ws, stream=Stream())
     assert all(torch.equal(a, b) for a, b in zip(c.parts(raw), want)) and torch.equal(got, dw)
     assert alive == [[True] * 3] * 2
+
+
+def test_calls_behind_two_branches_of_a_graph():
+    """A captured call whose stream has just joined another branch waits for
+    both: its rows come from one, its weights from the other; and a call in a
+    branch of its own runs beside the first."""
+    c = Case((8, 16, 16), 4, 64, "bf16", box=(2, 4, 4), seed=31)
+    raw, g = torch.zeros_like(c.qkv), torch.zeros((2, c.d), device="cuda")
+    rows, weights = V.Act8.empty(raw.shape, c.d), V.Act8.empty(g.shape, c.d)
+    nr = V.NormRope(g[0], g[1], c.eps, c.table, c.dims)
+    one, two = ([c.token(), c.head(), c.head(), c.means()] for _ in range(2))
+    draw, dw = torch.zeros_like(raw), torch.zeros_like(g)
+    ws = torch.empty((V.qk_norm_rope_bwd_workspace_size(c.sh),), dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+
+    def passes():
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            V.act8_unpack(weights, g)
+        V.act8_unpack(rows, raw)
+        main.wait_stream(side)
+        V.qk_norm_rope_partition(c.sh, nr, raw, *one)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            V.qk_norm_rope_partition(c.sh, nr, rows, *two)
+        V.qk_norm_rope_bwd(c.sh, nr, raw, *c.grads, draw, dw, ws)
+        main.wait_stream(side)
+
+    def new(seed):
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        V.act8_pack(torch.randn(raw.shape, generator=gen, device="cuda").to(c.dt), rows)
+        V.act8_pack(1 + torch.randn((2, c.d), generator=gen, device="cuda"), weights)
+
+    new(1)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        passes()
+    every = [*one, *two, draw, dw]
+    for seed in (2, 3, 4):
+        new(seed)
+        graph.replay()
+        torch.cuda.synchronize()
+        kept = [t.clone() for t in every]
+        for t in (raw, g, *every):
+            t.zero_()
+        passes()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(kept, every))
+        want = [c.token(), c.head(), c.head(), c.means()]
+        V.qk_norm_rope_partition(c.sh, nr, raw, *want)
+        assert all(torch.equal(x, y) for x, y in zip(want, one))
