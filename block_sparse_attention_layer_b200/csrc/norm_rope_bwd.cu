@@ -7,8 +7,8 @@
 // the codes, whose squares sum to an exact integer, without their scales).
 //
 // Bound: HBM, 8 s n_h d elements (two of them 1.03 bytes when x is a
-// checkpoint).  12 heads of 128, bf16: 75600 tokens 286 to 297 us (0.97 to 1.00
-// of a plain copy's 6.46 TB/s), 55296 tokens 211 us, or from a checkpoint 194 to
+// checkpoint).  12 heads of 128, bf16: 75600 tokens 286 to 302 us by card (0.95 to
+// 1.00 of a plain copy's 6.46 TB/s), 55296 tokens 211 us, or from a checkpoint 194 to
 // 205 us (0.91 to 0.95; 2.4 instructions a cycle and SM).
 //
 // As in the forward, a lane works on two rows of q, k (and v) at a time, two

@@ -47,7 +47,8 @@ class VMoBALayer:
         self.dv = torch.empty((s, h, d), dtype=dt, device=dev)
         # calls so far that wrote a part of the forward state in the buffers
         # (permuted keys and values, selection, pair lists, LSE, fp32 output
-        # copy): lets a caller tell whether that state is still its own
+        # copy): lets a caller tell whether that state is still its own.  A
+        # captured graph's replays write to the buffers without counting
         self.generation = 0
         self._device = dev
 

@@ -312,8 +312,10 @@ int vmoba_score_select_static(const vmoba_shape* shape, const void* q, const flo
 
 /* ---- Around the attention: norm + rotation, 8-bit checkpoints ----
  *
- * Between the projection and the attention a video DiT normalises each
- * head's query and key and rotates them by the token's position:
+ * Between the projection and the attention many video DiTs normalise each
+ * head's query and key on its own and rotate them by the token's position (a
+ * norm over all heads of a token together, with n_heads * head_dim weights, is
+ * not offered):
  *   norm:      y_i = x_i g_i / sqrt(mean_j x_j^2 + eps) over the head_dim
  *              values of one token and head;
  *   rotation:  the adjacent pairs (2p, 2p+1) turn by the angle
